@@ -24,6 +24,12 @@ MOE_Q4_1 = 3
 MOE_Q4_K = 12
 MOE_Q6_K = 14
 
+# activation types of the operators next to the step, and 4-bit rows held as planes
+MOE_F32 = 0
+MOE_F16 = 1
+MOE_BF16 = 30
+MOE_Q4_PLANES = 64
+
 MOE_ACCUMULATE = 1
 MOE_RESIDUAL = 2
 MOE_HOST_IO = 4
@@ -32,6 +38,8 @@ MOE_TRACE = 16
 MOE_BATCHED = 32
 MOE_F32_ACT = 64
 MOE_GRAPH = 128
+MOE_FRESH_STATE = 256
+MOE_TOKEN_DECAY = 512
 
 MOE_OK = 0
 MOE_ERR_INVALID_CFG = -1
@@ -47,7 +55,8 @@ NORM_MIN = 6.103515625e-05  # 2^-14
 # Every symbol include/moeffn.h declares.
 EXPORTS = ("moe_ffn_forward", "moe_ffn_forward_ex", "moe_workspace_size", "moe_trace_offset",
            "moe_workspace_status", "moe_selftest_timeout", "moe_ffn_forward_noalloc", "moe_last_error",
-           "moe_shutdown")
+           "moe_shutdown", "moe_q4_matvec", "moe_linattn_prefill", "moe_linattn_workspace_size",
+           "moe_linattn_step")
 
 
 class moe_cfg(ctypes.Structure):
@@ -83,6 +92,56 @@ def make_cfg(hidden, n_experts, top_k, expert_ff, shared_ff=0, n_groups=1, group
                    rms_eps, _ptr(ffn_norm), qtype_down or 0)
 
 
+class moe_matvec_cfg(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("n_vec", ctypes.c_int32),
+        ("qtype", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("x_type", ctypes.c_int32),
+        ("y_type", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+    ]
+
+
+def make_matvec_cfg(rows, cols, n_vec=1, qtype=MOE_Q4_1, group=0, x_type=MOE_F32, y_type=MOE_F32, flags=0,
+                    x_stride=0, y_stride=0):
+    """A :class:`moe_matvec_cfg`; strides in values, 0 for packed vectors."""
+    return moe_matvec_cfg(rows, cols, n_vec, qtype, group, x_type, y_type, flags, x_stride, y_stride)
+
+
+class moe_linattn_cfg(ctypes.Structure):
+    _fields_ = [
+        ("n_seq", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("n_qk_heads", ctypes.c_int32),
+        ("key_dim", ctypes.c_int32),
+        ("value_dim", ctypes.c_int32),
+        ("n_states", ctypes.c_int32),
+        ("type", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("o_stride", ctypes.c_int64),
+    ]
+
+
+def make_linattn_cfg(n_seq, n_tokens, n_heads, key_dim, value_dim, n_qk_heads=None, n_states=None, type=MOE_BF16,
+                     scale=None, flags=0, q_stride=0, k_stride=0, v_stride=0, o_stride=0):
+    """A :class:`moe_linattn_cfg`. Defaults: as many q/k heads as heads, a state for each
+    sequence, scale ``key_dim ** -0.5``, packed tokens (strides in values)."""
+    return moe_linattn_cfg(n_seq, n_tokens, n_heads, n_heads if n_qk_heads is None else n_qk_heads, key_dim,
+                           value_dim, n_seq if n_states is None else n_states, type,
+                           key_dim ** -0.5 if scale is None else scale, flags, q_stride, k_stride, v_stride,
+                           o_stride)
+
+
 class MoeError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"moeffn error {code}: {msg}")
@@ -114,6 +173,15 @@ def lib():
         L.moe_selftest_timeout.restype = ctypes.c_int
         L.moe_ffn_forward_noalloc.argtypes = [vp, vp, vp, vp, vp, cp, vp, vp]
         L.moe_ffn_forward_noalloc.restype = ctypes.c_int
+        mp, ap = ctypes.POINTER(moe_matvec_cfg), ctypes.POINTER(moe_linattn_cfg)
+        L.moe_q4_matvec.argtypes = [vp, vp, vp, vp, vp, mp, vp, vp]
+        L.moe_q4_matvec.restype = ctypes.c_int
+        L.moe_linattn_prefill.argtypes = [vp, vp, vp, vp, vp, vp, ap, vp, vp, vp, ctypes.c_size_t, vp]
+        L.moe_linattn_prefill.restype = ctypes.c_int
+        L.moe_linattn_workspace_size.argtypes = [ap]
+        L.moe_linattn_workspace_size.restype = ctypes.c_size_t
+        L.moe_linattn_step.argtypes = [vp, vp, vp, vp, vp, ap, vp, vp, vp]
+        L.moe_linattn_step.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_shutdown.argtypes = []
@@ -184,6 +252,26 @@ def moe_ffn_forward_noalloc(x, router_w, router_bias, expert_blocks, shared_bloc
     """The step without any allocation (fixed 512 KiB device scratch; blocking)."""
     return lib().moe_ffn_forward_noalloc(_ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(expert_blocks),
                                          _ptr(shared_blocks), ctypes.byref(cfg), _ptr(out), _stream(stream))
+
+
+def moe_q4_matvec(x, weights, scales, mins, bias, cfg, y, stream=None):
+    return lib().moe_q4_matvec(_ptr(x), _ptr(weights), _ptr(scales), _ptr(mins), _ptr(bias), ctypes.byref(cfg),
+                               _ptr(y), _stream(stream))
+
+
+def moe_linattn_prefill(q, k, v, log_decay, offsets, slots, cfg, state, o, workspace, workspace_bytes, stream=None):
+    return lib().moe_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(offsets), _ptr(slots),
+                                     ctypes.byref(cfg), _ptr(state), _ptr(o), _ptr(workspace),
+                                     int(workspace_bytes), _stream(stream))
+
+
+def moe_linattn_workspace_size(cfg):
+    return lib().moe_linattn_workspace_size(ctypes.byref(cfg))
+
+
+def moe_linattn_step(q, k, v, log_decay, slots, cfg, state, o, stream=None):
+    return lib().moe_linattn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), ctypes.byref(cfg),
+                                  _ptr(state), _ptr(o), _stream(stream))
 
 
 def moe_last_error():

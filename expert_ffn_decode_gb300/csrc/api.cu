@@ -11,6 +11,7 @@
 #include "../../include/moeffn.h"
 #include "common.cuh"
 #include "decode_host.h"
+#include "ops_host.h"
 #include "plan.h"
 #include "prefill_host.h"
 
@@ -31,6 +32,23 @@ int cuda_fail(cudaError_t e, const char* what) {
   cudaGetLastError();  // clear the sticky launch error, if any
   return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+}  // namespace
+
+// The same error text for the entry points in other files.
+namespace moe {
+int set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+int set_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+void clear_error() { g_err[0] = 0; }
+}  // namespace moe
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -71,6 +71,13 @@ extern "C" {
 #define MOE_Q4_K 12
 #define MOE_Q6_K 14
 
+/* Activation types of the operators next to the step (ggml type ids). */
+#define MOE_F32 0
+#define MOE_F16 1
+#define MOE_BF16 30
+/* 4-bit rows held as separate planes, for moe_q4_matvec (not a ggml type). */
+#define MOE_Q4_PLANES 64
+
 /* moe_cfg.flags */
 #define MOE_ACCUMULATE 1u /* out = out + contribution (the pages' x += ...)          */
 #define MOE_RESIDUAL 2u   /* out = x + contribution                                 */
@@ -256,6 +263,104 @@ int moe_selftest_timeout(void* workspace, void* stream);
 int moe_ffn_forward_noalloc(const float* x, const float* router_w, const float* router_bias,
                             const void* expert_blocks, const void* shared_blocks, const moe_cfg* cfg,
                             float* out, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators next to the step: the projections of a layer whose matrices are 4-bit blocks,
+ * and linear attention with a decay for each head. With the step they make a whole
+ * recurrent layer: projection, moe_linattn_prefill or moe_linattn_step, projection added
+ * into the residual stream, moe_ffn_forward_ex with the norm prologue and MOE_RESIDUAL
+ * (examples/linear_layer.py).
+ * ------------------------------------------------------------------------------------- */
+
+/* moe_linattn_cfg.flags (besides MOE_NO_PDL) */
+#define MOE_FRESH_STATE 256u /* sequences start from a zero state: the pool is only written */
+#define MOE_TOKEN_DECAY 512u /* log_decay has a row for each token                          */
+
+/* A matrix W [rows][cols] and the vectors it multiplies.
+ *   qtype MOE_Q4_0, MOE_Q4_1, MOE_Q4_K: rows of blocks as in the expert records above
+ *     (cols a multiple of 32, of 256 for MOE_Q4_K), group 0.
+ *   qtype MOE_Q4_PLANES: `weights` is [rows][cols / 2] nibble bytes, 16 bytes for every 32
+ *     values in the blocks' order (byte i: value i low, value 16 + i high); `scales` is
+ *     [rows][cols / group] f16 and `mins` the same or NULL, group 32, 64 or 128, dividing
+ *     cols; value = scale q + min, without mins scale (q - 8).
+ * Limits: 1 <= rows; 32 <= cols <= 16384; n_vec >= 0 (0: nothing is launched). */
+typedef struct moe_matvec_cfg {
+  int32_t rows;
+  int32_t cols;
+  int32_t n_vec;
+  int32_t qtype;
+  int32_t group;
+  int32_t x_type;   /* MOE_F32, MOE_F16 or MOE_BF16 */
+  int32_t y_type;
+  uint32_t flags;   /* MOE_ACCUMULATE (y = y + ...), MOE_NO_PDL */
+  int64_t x_stride; /* values from one vector to the next; 0: cols */
+  int64_t y_stride; /* 0: rows */
+} moe_matvec_cfg;
+
+/* y_t = W x_t (+ bias) (+ y_t) for n_vec vectors, enqueued on `stream`. `bias` is [rows] f32
+ * or NULL; scales and mins are NULL unless qtype is MOE_Q4_PLANES. No workspace. Sums are
+ * f32 or wider whatever the types, y is rounded once, and repeat calls agree bit for bit. Each
+ * vector's result does not depend on the others of the call. A vector that holds an
+ * infinity or a NaN gives rows that are not finite.
+ * The matrix is read before the previous kernel on the stream has finished, as the step
+ * reads its weights, unless MOE_NO_PDL is set. Alignment: weights, scales, mins, x and every
+ * vector of x (x_stride) 16 bytes; y and bias their element. x and y must not overlap. */
+int moe_q4_matvec(const void* x, const void* weights, const void* scales, const void* mins, const float* bias,
+                  const moe_matvec_cfg* cfg, void* y, void* stream);
+
+/* Linear attention with a decay for each head. For each sequence and each of n_heads heads
+ * the state S is key_dim x value_dim, and token t does
+ *   S = exp(g_t) S + k_t v_t^T,   o_t = scale * S^T q_t
+ * (the token's own k and v included). Layouts, all row-major:
+ *   q, k       [n_tokens][n_qk_heads][key_dim]; head h reads q/k head h / (n_heads / n_qk_heads)
+ *   v, o       [n_tokens][n_heads][value_dim]
+ *   log_decay  g, f32: [n_heads], or [n_tokens][n_heads] with MOE_TOKEN_DECAY. -infinity
+ *              forgets the state before the token.
+ *   state      [n_states][n_heads][key_dim][value_dim] f32, updated in place
+ *   slots      [n_seq] int32, the state of each sequence, or NULL for sequence b in state b.
+ *              A sequence whose slot is outside 0 .. n_states - 1 is inactive: its rows of o
+ *              become 0 and no state is touched. Two sequences must not share a slot.
+ * q, k, v and o have one type; tokens may be strided (views of one projected buffer).
+ * Limits: key_dim and value_dim multiples of 8 from 8 to 128; n_qk_heads divides n_heads,
+ * n_heads <= 1024; n_seq <= 65535; n_seq and n_tokens >= 0; scale finite. Alignment: q, k,
+ * v, o, state and every token row (strides) 16 bytes, the others 4. o must not overlap
+ * q, k or v. */
+typedef struct moe_linattn_cfg {
+  int32_t n_seq;
+  int32_t n_tokens;  /* of all sequences together; a step has n_tokens == n_seq */
+  int32_t n_heads;
+  int32_t n_qk_heads;
+  int32_t key_dim;
+  int32_t value_dim;
+  int32_t n_states;
+  int32_t type;      /* of q, k, v, o: MOE_F32, MOE_F16 or MOE_BF16 */
+  float scale;
+  uint32_t flags;    /* MOE_FRESH_STATE, MOE_TOKEN_DECAY, MOE_NO_PDL */
+  int64_t q_stride;  /* values from one token to the next; 0: packed */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t o_stride;
+} moe_linattn_cfg;
+
+/* Whole prompts: sequence b is the tokens offsets[b] .. offsets[b + 1] - 1 (device int32,
+ * n_seq + 1 values, ascending; bounds outside 0 .. n_tokens are clamped to it and a
+ * descending pair is an empty sequence). offsets NULL: n_seq sequences of n_tokens / n_seq
+ * tokens. An empty sequence keeps its state (or gets a zero one with MOE_FRESH_STATE).
+ * Rows of o that no sequence covers are not written. `workspace` as for
+ * moe_ffn_forward_ex (zero-filled before its first use, then this library's), of at
+ * least moe_linattn_workspace_size(cfg) bytes; a wait that gave up surfaces through
+ * moe_workspace_status. */
+int moe_linattn_prefill(const void* q, const void* k, const void* v, const float* log_decay,
+                        const int32_t* offsets, const int32_t* slots, const moe_linattn_cfg* cfg, float* state,
+                        void* o, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a moe_linattn_prefill call (0 for an invalid cfg). */
+size_t moe_linattn_workspace_size(const moe_linattn_cfg* cfg);
+
+/* One token for each sequence (row b of q, k, v, o and of a per-token log_decay is
+ * sequence b). No workspace. */
+int moe_linattn_step(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* slots,
+                     const moe_linattn_cfg* cfg, float* state, void* o, void* stream);
 
 /* Text of the last error on the calling thread ("" if none). */
 const char* moe_last_error(void);
