@@ -3,28 +3,10 @@
 //   S = exp(g_t) S + k_t v_t^T,   o_t = scale * S^T q_t.
 //
 // lin_scan walks a sequence's tokens in turn with the state in registers.
-#include "common.cuh"
-#include "ops_host.h"
-#include "types.cuh"
+#include "linattn.cuh"
 
 namespace moe {
 namespace {
-
-// Tokens begin .. end - 1 of sequence b (clamped to the call's tokens; descending: empty).
-__device__ __forceinline__ void seq_range(const LinattnArgs& a, int b, int& begin, int& end) {
-  if (a.offsets) {
-    begin = min(max(a.offsets[b], 0), a.N);
-    end = max(min(max(a.offsets[b + 1], 0), a.N), begin);
-  } else {
-    begin = b * a.seq_len;
-    end = begin + a.seq_len;
-  }
-}
-// The state of sequence b, or -1 when the sequence is inactive.
-__device__ __forceinline__ int seq_slot(const LinattnArgs& a, int b) {
-  const int s = a.slots ? a.slots[b] : b;
-  return s >= 0 && s < a.n_states ? s : -1;
-}
 
 constexpr int SCAN_TOK = 16;  // tokens staged at a time
 
@@ -102,13 +84,14 @@ cudaError_t scan_launch(const LinattnArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t linattn_prefill_launch(const LinattnArgs& a, int type, void* ws, bool pdl, cudaStream_t st) {
-  if (type == MOE_F32) return scan_launch<float>(a, st);
-  if (type == MOE_F16) return scan_launch<__half>(a, st);
-  return scan_launch<__nv_bfloat16>(a, st);
+  if (a.N > 48) return linattn_chunk_launch(a, type, ws, pdl, st);
+  return linattn_step_launch(a, type, pdl, st);
 }
 
 cudaError_t linattn_step_launch(const LinattnArgs& a, int type, bool pdl, cudaStream_t st) {
-  return linattn_prefill_launch(a, type, nullptr, pdl, st);  // one token a sequence: seq_len is 1
+  if (type == MOE_F32) return scan_launch<float>(a, st);
+  if (type == MOE_F16) return scan_launch<__half>(a, st);
+  return scan_launch<__nv_bfloat16>(a, st);
 }
 
 }  // namespace moe

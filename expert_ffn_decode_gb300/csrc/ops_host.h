@@ -45,6 +45,33 @@ struct LinattnArgs {
   float scale;
   int fresh, token_decay;
 };
+// How a prompt call is cut: sequences into units of `seg` tokens (a multiple of 64), so that
+// units x heads fill the GPU's 304 CTA places about once (152 SMs, two CTAs each); at least
+// LINATTN_MIN_SEG tokens, since a cut costs a second pass over k and v and a state's round
+// trip. `units` bounds their number from what the host knows, `n_ws` the states that
+// sequences of several units keep in the workspace; the rest are byte offsets in it.
+constexpr int LINATTN_MIN_SEG = 256;
+struct LinattnSplit {
+  int seg, units, n_ws;
+  size_t decays, states, total;
+};
+inline LinattnSplit linattn_split(int N, int B, int H, int dk, int dv) {
+  LinattnSplit s{};
+  const int want = 304 / H > 1 ? 304 / H : 1;
+  int64_t seg = ((int64_t)N + want - 1) / want;
+  seg = (seg + 63) / 64 * 64;
+  if (seg < LINATTN_MIN_SEG) seg = LINATTN_MIN_SEG;
+  s.seg = seg > 1 << 30 ? 1 << 30 : (int)seg;
+  s.units = N / s.seg + B;       // sum of ceil(n_b / seg), an empty sequence counting one
+  s.n_ws = 2 * (N / s.seg);      // a sequence longer than seg has at most 2 n_b / seg units
+  size_t o = 512;
+  s.decays = o;
+  o = (o + (size_t)s.n_ws * H * 4 + 255) / 256 * 256;
+  s.states = o;
+  o = (o + (size_t)s.n_ws * H * dk * dv * 4 + 255) / 256 * 256;
+  s.total = o;
+  return s;
+}
 cudaError_t linattn_prefill_launch(const LinattnArgs& a, int type, void* ws, bool pdl, cudaStream_t st);
 cudaError_t linattn_step_launch(const LinattnArgs& a, int type, bool pdl, cudaStream_t st);
 
