@@ -154,6 +154,23 @@ __device__ __forceinline__ void read_piece(const uint8_t* p, float (&x)[8]) {
   }
 }
 
+// The products of parts i < NA of one operand and j < NB of the other with i + j <= LIM, each
+// in KS steps of 16 along K: the smallest first, because the tensor core's accumulator
+// loses up to a last bit with every step, of what it holds by then.
+template <int NA, int NB, int LIM, int KS, typename F>
+__device__ __forceinline__ void each_product(F f) {
+  bool first = true;
+#pragma unroll
+  for (int sum = LIM; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (i + j == sum)
+#pragma unroll
+          for (int s = 0; s < KS; ++s, first = false) f(i, j, s, first);
+}
+
 // The chunk's decays, by one warp (lane: tokens 2 lane, 2 lane + 1). Sums are carried as an
 // f32 value and its rounding error, in powers of two, so that G_t - G_s keeps f32 accuracy
 // however far down the chunk has decayed. A g below -104 (exp(g) < 2^-150, 0 in f32) is a
@@ -356,18 +373,14 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
 
     // ---- scores and the state's share ----------------------------------------------
     if (MODE == 1 && tid == 0) {
-      bool first = true;
-      for (int i = 0; i < NP; ++i)
-        for (int j = 0; j < NP && i + j <= LIM; ++j)
-          for (int s = 0; s < D / 16; ++s, first = false)
-            mma_f16(tm + L::T_O1, smem_desc(sm + L::Q + i * TILE + s * 2048, 1024, 128),
-                    smem_desc(sm + L::K + j * TILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 0, 0), !first);
-      first = true;
-      for (int i = 0; i < NPP; ++i)
-        for (int j = 0; j < NP && i + j <= LIM; ++j)
-          for (int s = 0; s < D / 16; ++s, first = false)
-            mma_ts(tm + L::T_O2, tm + L::T_S + i * 64 + s * 8,
-                   smem_desc(sm + L::Q + j * TILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 0, 0), !first);
+      each_product<NP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+        mma_f16(tm + L::T_O1, smem_desc(sm + L::Q + i * TILE + s * 2048, 1024, 128),
+                smem_desc(sm + L::K + j * TILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 0, 0), !first);
+      });
+      each_product<NPP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+        mma_ts(tm + L::T_O2, tm + L::T_S + i * 64 + s * 8, smem_desc(sm + L::Q + j * TILE + s * 2048, 1024, 128),
+               idesc_bf16(128, CH, 0, 0), !first);
+      });
       mma_commit(&m->bar);
     }
     // the decayed keys, three parts
@@ -426,12 +439,10 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
       tc_fence_after_sync();
       // ---- the chunk's own share --------------------------------------------------
       if (tid == 0) {
-        bool first = true;
-        for (int i = 0; i < NP; ++i)
-          for (int j = 0; j < NPP && i + j <= LIM; ++j)
-            for (int s = 0; s < CH / 16; ++s, first = false)
-              mma_f16(tm + L::T_O1, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
-                      smem_desc(sm + L::P + j * PTILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 1, 0), !first);
+        each_product<NP, NPP, LIM, CH / 16>([&](int i, int j, int s, bool first) {
+          mma_f16(tm + L::T_O1, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
+                  smem_desc(sm + L::P + j * PTILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 1, 0), !first);
+        });
         mma_commit(&m->bar);
       }
       ok = mbar_wait(&m->bar, phase) && ok;
@@ -457,12 +468,10 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
     __syncthreads();
     tc_fence_after_sync();
     if (tid == 0) {
-      bool first = true;
-      for (int i = 0; i < NP; ++i)
-        for (int j = 0; j < 3 && i + j <= 2; ++j)
-          for (int s = 0; s < CH / 16; ++s, first = false)
-            mma_f16(tm + L::T_A, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
-                    smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024), idesc_bf16(128, D, 1, 1), !first);
+      each_product<NP, 3, 2, CH / 16>([&](int i, int j, int s, bool first) {
+        mma_f16(tm + L::T_A, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
+                smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024), idesc_bf16(128, D, 1, 1), !first);
+      });
       mma_commit(&m->bar);
     }
     ok = mbar_wait(&m->bar, phase) && ok;
