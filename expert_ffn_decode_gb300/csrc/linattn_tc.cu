@@ -27,33 +27,40 @@ namespace {
 constexpr int CH = 64;                  // tokens of a chunk
 constexpr int D = 128;                  // key and value width of the tiles (narrower ones are zero-filled)
 constexpr uint32_t TILE = CH * D * 2;   // one part of a [64][128] operand
-constexpr uint32_t PTILE = CH * CH * 2; // one part of the scores
+// One part of the scores, without what the mask leaves empty: the 16 columns s = 16 i .. of
+// step i of the product over s are kept for the rows t >= 16 i.
+constexpr uint32_t PTILE = 5120;
+__host__ __device__ constexpr uint32_t p_base(int i) { return 32u * (64 * i - 8 * i * (i - 1)); }
+__host__ __device__ constexpr uint32_t p_pitch(int i) { return 16u * (64 - 16 * i); }  // from 8 columns to the next 8
 
 template <int NP>
 struct Plan {
   static constexpr int NPP = NP == 3 ? 3 : 2;  // parts of scores and state operands
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
-  static constexpr uint32_t P = K;             // the scores take the keys' place once those are used
-  static constexpr uint32_t MISC = KT + 3 * TILE;
-  static constexpr uint32_t BYTES = MISC + 3072;
-  // tensor memory columns: accumulators (scores then O1 | O2; later A), then the state's parts
-  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_A = 0, T_S = 128;
+  static constexpr uint32_t P = KT + 3 * TILE;
+  static constexpr uint32_t MISC = P + NPP * PTILE;
+  static constexpr uint32_t BYTES = MISC + 3584;  // bf16: 112,128 bytes, two CTAs an SM
+  // tensor memory columns: scores then O1, O2, and the state's parts, whose place A takes
+  // once O2 is done
+  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128;
   static constexpr uint32_t T_COLS = NP == 3 ? 512 : 256;
 };
 
-struct Misc {
+struct Decays {
   float4 g[CH];      // G_t in powers of two: sum's high and low part, resets so far, exp(g_t)
   float w[CH];       // exp(G_63 - G_s)
   float eg[CH];      // exp(G_t)
   float lam;         // exp(G_63)
   float ghi, glo;    // sum over the chunk without resets
   int reset;         // whether the chunk forgets
-  uint32_t tmem;
-  uint32_t pad;
+};
+struct Misc {
+  Decays d[2];       // of this chunk and the next
   uint64_t bar;
+  uint32_t tmem;
   int scratch[4 + 16];
 };
-static_assert(sizeof(Misc) <= 3072, "misc");
+static_assert(sizeof(Misc) <= 3584, "misc");
 
 // bf16 K-major (bit 0) or MN-major (1) operands, f32 accumulator, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int ta, int tb) {
@@ -107,38 +114,64 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t u) { return ((u & 0x7f80
 // along K, 128 along rows) and as an MN-major one (rows along K: 128 along K, 1024 along columns).
 __device__ __forceinline__ uint32_t piece(int kc, int row) { return (uint32_t)(kc * CH + row) * 16u; }
 
-// Loads rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] matrix as NP parts. A thread
-// takes 8-column pieces of one row; a warp's 32 pieces are 64 contiguous bytes (16-bit types)
-// of 8 rows and fill four whole 128-byte lines of shared memory.
+// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] matrix: four
+// 8-column pieces of one row. A warp's 32 pieces of one i are 64 contiguous bytes (16-bit
+// types) of 8 rows and fill four whole 128-byte lines of shared memory. One bf16 part goes
+// to shared memory as it is, asynchronously; other types pass through registers (fetch early,
+// put when the tile is free).
 template <typename T, int NP>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const T* src, int64_t stride, int t0, int n, int dim) {
-  const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+struct Loader {
+  static constexpr int W = NP == 1 ? 1 : sizeof(T) * 2;  // 32-bit words of a piece held here
+  uint32_t r[D / 32][W];
+  __device__ __forceinline__ void fetch(uint8_t* dst, const T* src, int64_t stride, int t0, int n, int dim) {
+    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int kc = i * 4 + (lane >> 3);
-    const bool in = row < n && kc * 8 < dim;
-    const T* p = in ? src + (t0 + row) * stride + kc * 8 : src;
-    uint8_t* d = dst + piece(kc, row);
-    if constexpr (NP == 1) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(d)), "l"(p), "r"(in ? 16 : 0)
-                   : "memory");
-    } else {
-      uint32_t u[NP][4];
+    for (int i = 0; i < D / 32; ++i) {
+      const int kc = i * 4 + (lane >> 3);
+      const bool in = row < n && kc * 8 < dim;
+      const T* p = in ? src + (t0 + row) * stride + kc * 8 : src;
+      if constexpr (NP == 1) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst + piece(kc, row))), "l"(p),
+                     "r"(in ? 16 : 0)
+                     : "memory");
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 x = in ? load4(p + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        uint32_t a[NP], b[NP];
-        split_pair<NP>(x.x, x.y, a);
-        split_pair<NP>(x.z, x.w, b);
-#pragma unroll
-        for (int q = 0; q < NP; ++q) u[q][2 * j] = a[q], u[q][2 * j + 1] = b[q];
+        for (int j = 0; j < W / 4; ++j) {
+          const uint4 u = in ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
+          r[i][4 * j] = u.x;
+          r[i][4 * j + 1] = u.y;
+          r[i][4 * j + 2] = u.z;
+          r[i][4 * j + 3] = u.w;
+        }
       }
-#pragma unroll
-      for (int q = 0; q < NP; ++q)
-        *reinterpret_cast<uint4*>(d + q * TILE) = make_uint4(u[q][0], u[q][1], u[q][2], u[q][3]);
     }
   }
+  __device__ __forceinline__ void put(uint8_t* dst) const {
+    if constexpr (NP > 1) {
+      const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t u[4][NP];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x;
+          if constexpr (sizeof(T) == 4) x = make_float2(__uint_as_float(r[i][2 * j]), __uint_as_float(r[i][2 * j + 1]));
+          else x = __half22float2(*reinterpret_cast<const __half2*>(&r[i][j]));
+          split_pair<NP>(x.x, x.y, u[j]);
+        }
+        uint8_t* d = dst + piece(i * 4 + (lane >> 3), row);
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+          *reinterpret_cast<uint4*>(d + q * TILE) = make_uint4(u[0][q], u[1][q], u[2][q], u[3][q]);
+      }
+    }
+  }
+};
+template <int pending>
+__device__ __forceinline__ void copies_wait() {  // all but the last `pending` groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(pending) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Eight values of a piece, the parts added up (exact: they do not overlap).
 template <int NP>
 __device__ __forceinline__ void read_piece(const uint8_t* p, float (&x)[8]) {
@@ -175,7 +208,7 @@ __device__ __forceinline__ void each_product(F f) {
 // f32 value and its rounding error, in powers of two, so that G_t - G_s keeps f32 accuracy
 // however far down the chunk has decayed. A g below -104 (exp(g) < 2^-150, 0 in f32) is a
 // reset: it is counted instead of added, and tokens on two sides of one do not meet.
-__device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0, int n, Misc* m) {
+__device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0, int n, Decays* m) {
   const int lane = threadIdx.x & 31;
   float raw[2], hi[2], lo[2];
   int r[2];
@@ -310,67 +343,90 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
   bool ok = true;
   float sum_hi = 0.f, sum_lo = 0.f;
   int resets = 0;
-  for (int t0 = begin; t0 < end && ok; t0 += CH) {
+  Loader<T, NP> lq, lk, lv;
+  auto fetch_qk = [&](int t0) {
     const int n = min(CH, end - t0);
-    // ---- operands ----------------------------------------------------------------
-    if (MODE == 1) load_tile<T, NP>(sm + L::Q, q, a.qs, t0, n, a.dk);
-    load_tile<T, NP>(sm + L::K, k, a.ks, t0, n, a.dk);
-    load_tile<T, NP>(sm + L::V, v, a.vs, t0, n, a.dv);
-    if (warp == 0) chunk_decays(a, h, t0, n, m);
-    if constexpr (NP == 1) asm volatile("cp.async.wait_all;" ::: "memory");
-    uint32_t bad = 0;  // an infinity or NaN among this thread's pieces of v
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(sm + L::V + piece(i * 4 + (lane >> 3), warp * 8 + (lane & 7)));
-      bad |= non_finite(u.x) | non_finite(u.y) | non_finite(u.z) | non_finite(u.w);
+    if (t0 < end) {
+      if (MODE == 1) lq.fetch(sm + L::Q, q, a.qs, t0, n, a.dk);
+      lk.fetch(sm + L::K, k, a.ks, t0, n, a.dk);
     }
-    fence_proxy_async_smem();
-    const bool scalar = __syncthreads_or(bad != 0);
-    tc_fence_after_sync();
-    sum_lo += m->glo;
-    {
-      const float s = sum_hi + m->ghi, bb = s - sum_hi;
-      sum_lo += (sum_hi - (s - bb)) + (m->ghi - bb);
-      sum_hi = s;
+    copies_commit();
+  };
+  auto put_qk = [&]() {
+    if (MODE == 1) lq.put(sm + L::Q);
+    lk.put(sm + L::K);
+  };
+  // the state before the products that read it, and the state after the chunk's share
+  auto add_state = [&](float lam) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[16];
+      tmem_ld16(tlane + L::T_A + wg * 64 + c * 16, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) S[c * 16 + j] = fmaf(lam, S[c * 16 + j], __uint_as_float(r[j]));
     }
-    resets |= m->reset;
-
-    if (scalar) {
-      // A masked product with an infinity or a NaN is a NaN, which would reach the chunk's
-      // earlier tokens: such a chunk goes token by token.
-      float* part = reinterpret_cast<float*>(sm + L::KT);
-      for (int t = 0; t < n; ++t) {
-        float vv = 0.f;
-        for (int p = NP - 1; p >= 0; --p) {
-          const uint16_t b = *reinterpret_cast<const uint16_t*>(sm + L::V + p * TILE + piece(row >> 3, t) + (row & 7) * 2);
-          const float x = __uint_as_float((uint32_t)b << 16);
-          vv = p == NP - 1 || isfinite(x) ? vv + x : x;  // an infinity has no lower parts
-        }
-        const float lam = m->g[t].w;
-        float acc = 0.f;
+  };
+  // A masked product with an infinity or a NaN is a NaN, which would reach the chunk's earlier
+  // tokens: a chunk whose v holds one goes token by token, from global memory.
+  auto token_by_token = [&](int t0, int n, const Decays* d) {
+    float* part = reinterpret_cast<float*>(sm + L::V);
+    for (int t = 0; t < n; ++t) {
+      const float vv = row < a.dv ? to_f32(v[(t0 + t) * a.vs + row]) : 0.f;
+      const float lam = d->g[t].w;
+      float acc = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float kk[8], qq[8];
-          read_piece<NP>(sm + L::K + piece(wg * 8 + c, t), kk);
-          if (MODE == 1) read_piece<NP>(sm + L::Q + piece(wg * 8 + c, t), qq);
+      for (int c = 0; c < 16; ++c) {
+        const int at = wg * 64 + c * 4;
+        if (at < a.dk) {
+          const float4 kk = load4(k + (t0 + t) * a.ks + at);
+          const float4 qq = MODE == 1 ? load4(q + (t0 + t) * a.qs + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, q4[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            S[c * 8 + j] = fmaf(lam, S[c * 8 + j], kk[j] * vv);
-            if (MODE == 1) acc = fmaf(qq[j], S[c * 8 + j], acc);
+          for (int j = 0; j < 4; ++j) {
+            S[c * 4 + j] = fmaf(lam, S[c * 4 + j], k4[j] * vv);
+            acc = fmaf(q4[j], S[c * 4 + j], acc);
           }
         }
-        if (MODE == 1) {
-          if (wg == 1) part[row] = acc;
-          __syncthreads();
-          if (wg == 0 && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>((acc + part[row]) * a.scale);
-          __syncthreads();
-        }
       }
-      __syncthreads();
-      if (MODE == 1) put_state();
-      continue;
+      if (MODE == 1) {
+        if (wg == 1) part[row] = acc;
+        __syncthreads();
+        if (wg == 0 && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>((acc + part[row]) * a.scale);
+        __syncthreads();
+      }
     }
+  };
+  auto v_non_finite = [&](const uint8_t* tile) {  // among this thread's own pieces
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(tile + piece(i * 4 + (lane >> 3), warp * 8 + (lane & 7)));
+      bad |= non_finite(u.x) | non_finite(u.y) | non_finite(u.z) | non_finite(u.w);
+    }
+    return bad != 0;
+  };
 
+  if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
+  fetch_qk(begin);
+  put_qk();
+  int buf = 0;
+  for (int t0 = begin; t0 < end && ok; t0 += CH, buf ^= 1) {
+    const int n = min(CH, end - t0);
+    const Decays* d = &m->d[buf];
+    copies_wait<0>();
+    fence_proxy_async_smem();
+    __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
+    tc_fence_after_sync();
+    lv.fetch(sm + L::V, v, a.vs, t0, n, a.dv);
+    copies_commit();
+    sum_lo += d->glo;
+    {
+      const float s = sum_hi + d->ghi, bb = s - sum_hi;
+      sum_lo += (sum_hi - (s - bb)) + (d->ghi - bb);
+      sum_hi = s;
+    }
+    resets |= d->reset;
     // ---- scores and the state's share ----------------------------------------------
     if (MODE == 1 && tid == 0) {
       each_product<NP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
@@ -388,7 +444,7 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
     for (int i = 0; i < D / 32; ++i) {
       const int r = warp * 8 + (lane & 7);
       const uint32_t at = piece(i * 4 + (lane >> 3), r);
-      const float w = m->w[r];
+      const float w = d->w[r];
       float x[8];
       read_piece<NP>(sm + L::K + at, x);
       uint32_t u[4][3];
@@ -398,76 +454,68 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
       for (int p = 0; p < 3; ++p)
         *reinterpret_cast<uint4*>(sm + L::KT + p * TILE + at) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
     }
-    fence_proxy_async_smem();
     if (MODE == 1) {
       ok = mbar_wait(&m->bar, phase);
       phase ^= 1;
       tc_fence_after_sync();
-      __syncthreads();  // every thread has read its keys: the scores may take their place
-      if (quarter < 2) {  // lanes 0 .. 63 hold the tokens' rows of scores
-        const float4 gt = m->g[row];
+    }
+    __syncthreads();  // q and k have been read: the next chunk's may come
+    fetch_qk(t0 + CH);
+    if (warp == 7 && t0 + CH < end) chunk_decays(a, h, t0 + CH, min(CH, end - t0 - CH), &m->d[buf ^ 1]);
+    if (MODE == 1 && quarter < 2 && wg <= quarter) {
+      // Lanes 0 .. 63 hold the tokens' rows of scores; columns 32 wg .. 32 wg + 31 here, of
+      // which the mask leaves none for rows below 32 and wg 1.
+      const float4 gt = d->g[row];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[16];
-          tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, s);
-          tmem_ld_wait();
+      for (int c = 0; c < 2; ++c) {
+        const int step = wg * 2 + c;  // of the product over s
+        uint32_t s[16];
+        tmem_ld16(tlane + L::T_O1 + step * 16, s);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t u[4][NPP];
+        for (int e = 0; e < 2; ++e) {
+          uint32_t u[4][NPP];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float p[2];
+          for (int j = 0; j < 4; ++j) {
+            float p[2];
 #pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                const int col = wg * 32 + c * 16 + e * 8 + 2 * j + f;
-                const float4 gs = m->g[col];
-                const float d = ex2((gt.x - gs.x) + (gt.y - gs.y));
-                p[f] = col <= row && gt.z == gs.z ? __uint_as_float(s[e * 8 + 2 * j + f]) * d : 0.f;
-              }
-              split_pair<NPP>(p[0], p[1], u[j]);
+            for (int f = 0; f < 2; ++f) {
+              const int col = step * 16 + e * 8 + 2 * j + f;
+              const float4 gs = d->g[col];
+              const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
+              p[f] = col <= row && gt.z == gs.z ? __uint_as_float(s[e * 8 + 2 * j + f]) * x : 0.f;
             }
+            split_pair<NPP>(p[0], p[1], u[j]);
+          }
+          if (row >= step * 16) {
 #pragma unroll
             for (int x = 0; x < NPP; ++x)
-              *reinterpret_cast<uint4*>(sm + L::P + x * PTILE + piece(wg * 4 + c * 2 + e, row)) =
-                  make_uint4(u[0][x], u[1][x], u[2][x], u[3][x]);
+              *reinterpret_cast<uint4*>(sm + L::P + x * PTILE + p_base(step) + e * p_pitch(step) +
+                                        (row - step * 16) * 16) = make_uint4(u[0][x], u[1][x], u[2][x], u[3][x]);
           }
         }
       }
-      fence_proxy_async_smem();
-      tc_fence_before_sync();
-      __syncthreads();
-      tc_fence_after_sync();
-      // ---- the chunk's own share --------------------------------------------------
-      if (tid == 0) {
-        each_product<NP, NPP, LIM, CH / 16>([&](int i, int j, int s, bool first) {
-          mma_f16(tm + L::T_O1, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
-                  smem_desc(sm + L::P + j * PTILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 1, 0), !first);
-        });
-        mma_commit(&m->bar);
-      }
-      ok = mbar_wait(&m->bar, phase) && ok;
-      phase ^= 1;
-      tc_fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o1[16], o2[16];
-        tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, o1);
-        tmem_ld16(tlane + L::T_O2 + wg * 32 + c * 16, o2);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = wg * 32 + c * 16 + j;
-          const float x = fmaf(m->eg[t], __uint_as_float(o2[j]), __uint_as_float(o1[j]));
-          if (t < n && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>(x * a.scale);
-        }
-      }
     }
-    // ---- the state ------------------------------------------------------------------
-    const float lam = m->lam;
+    lv.put(sm + L::V);
+    copies_wait<1>();
+    fence_proxy_async_smem();
     tc_fence_before_sync();
-    __syncthreads();
+    if (__syncthreads_or(v_non_finite(sm + L::V))) {
+      token_by_token(t0, n, d);
+      put_qk();
+      if (MODE == 1) put_state();
+      ok = !__syncthreads_or(!ok);
+      continue;
+    }
     tc_fence_after_sync();
+    // ---- the chunk's own share, and what it adds to the state ------------------------------
     if (tid == 0) {
+      if (MODE == 1)
+        each_product<NP, NPP, LIM, CH / 16>([&](int i, int j, int s, bool first) {
+          mma_f16(tm + L::T_O1 + s * 16, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
+                  smem_desc(sm + L::P + j * PTILE + p_base(s), p_pitch(s), 128), idesc_bf16(128, CH - 16 * s, 1, 0),
+                  !first);
+        });
       each_product<NP, 3, 2, CH / 16>([&](int i, int j, int s, bool first) {
         mma_f16(tm + L::T_A, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
                 smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024), idesc_bf16(128, D, 1, 1), !first);
@@ -477,17 +525,41 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
     ok = mbar_wait(&m->bar, phase) && ok;
     phase ^= 1;
     tc_fence_after_sync();
+    add_state(d->lam);
+    if (MODE == 1) {
+      // outputs, a thread's row is one value channel: turned in v's place into rows of tokens
+      T* stage = reinterpret_cast<T*>(sm + L::V);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t r[16];
-      tmem_ld16(tlane + L::T_A + wg * 64 + c * 16, r);
-      tmem_ld_wait();
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o1[16], o2[16];
+        tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, o1);
+        tmem_ld16(tlane + L::T_O2 + wg * 32 + c * 16, o2);
+        tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) S[c * 16 + j] = fmaf(lam, S[c * 16 + j], __uint_as_float(r[j]));
+        for (int j = 0; j < 16; ++j) {
+          const int t = wg * 32 + c * 16 + j;
+          const float x = fmaf(d->eg[t], __uint_as_float(o2[j]), __uint_as_float(o1[j]));
+          stage[t * D + row] = from_f32<T>(x * a.scale);
+        }
+      }
     }
-    if (MODE == 1) put_state();
-    ok = !__syncthreads_or(!ok);  // also: the accumulators and tiles are free again
+    put_qk();
+    tc_fence_before_sync();
+    ok = !__syncthreads_or(!ok);
+    tc_fence_after_sync();
+    if (MODE == 1) {
+      put_state();
+      constexpr int PC = D * (int)sizeof(T) / 16;  // 16-byte pieces of a token's row
+#pragma unroll
+      for (int i = 0; i < CH * PC / 256; ++i) {
+        const int t = (i * 256 + tid) / PC, c = (i * 256 + tid) % PC;
+        if (t < n && c * (16 / (int)sizeof(T)) < a.dv)
+          *reinterpret_cast<uint4*>(o + (t0 + t) * a.os + c * (16 / sizeof(T))) =
+              *reinterpret_cast<const uint4*>(sm + L::V + (i * 256 + tid) * 16);
+      }
+    }
   }
+  copies_wait<0>();
   if (!ok && tid == 0) atomicOr(ctrl + CTRL_STATUS, DEV_ERR_MBAR_TIMEOUT);
   float* to = MODE == 0 ? mine + (int64_t)a.H * sz : pool;  // what a unit leaves is the next one's start
   if (ok && (MODE == 0 || end == last)) {
