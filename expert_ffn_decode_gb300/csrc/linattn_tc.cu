@@ -18,6 +18,9 @@
 // as an operand keep two parts (16 bits) for 16-bit outputs and three for f32; the decayed
 // keys keep three always, because they are summed into the f32 state. Products of parts
 // below the last kept bit are left out. Sums, statistics and the state itself are f32.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "linattn.cuh"
 #include "tc.cuh"
 
@@ -39,10 +42,11 @@ struct Plan {
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
   static constexpr uint32_t P = KT + 3 * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
-  static constexpr uint32_t BYTES = MISC + 3584;  // bf16: 112,128 bytes, two CTAs an SM
-  // tensor memory columns: scores then O1, O2, and the state's parts, whose place A takes
-  // once O2 is done
-  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128;
+  static constexpr uint32_t BYTES = MISC + 4096;  // bf16: 112,640 bytes and 1,024 of slack, two CTAs an SM
+  // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
+  // their place once O2 is done where there are two of them (a thread's columns of A are its
+  // columns of the parts).
+  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = NP == 3 ? 320 : 128;
   static constexpr uint32_t T_COLS = NP == 3 ? 512 : 256;
 };
 
@@ -50,17 +54,21 @@ struct Decays {
   float4 g[CH];      // G_t in powers of two: sum's high and low part, resets so far, exp(g_t)
   float w[CH];       // exp(G_63 - G_s)
   float eg[CH];      // exp(G_t)
+  float ieg[CH];     // exp(-G_t), where `mild`
   float lam;         // exp(G_63)
   float ghi, glo;    // sum over the chunk without resets
   int reset;         // whether the chunk forgets
+  int mild;          // no resets, and every exp(G_t) within 2^-80 .. 2^20
+  int pad[3];
 };
 struct Misc {
   Decays d[2];       // of this chunk and the next
-  uint64_t bar;
+  uint64_t full_q, full_k, full_v;  // a tile has landed
+  uint64_t qk, qs, end;             // products are done
   uint32_t tmem;
   int scratch[4 + 16];
 };
-static_assert(sizeof(Misc) <= 3584, "misc");
+static_assert(sizeof(Misc) <= 4096, "misc");
 
 // bf16 K-major (bit 0) or MN-major (1) operands, f32 accumulator, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int ta, int tb) {
@@ -89,6 +97,44 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Operand descriptors of a [64][128] tile, for step s of 16 along K. A tile of one bf16 part
+// comes by TMA as two halves of 64 columns, rows of 128 bytes in the 128-byte swizzle; tiles of
+// several parts and the decayed keys are written by threads as core matrices without one.
+__device__ __forceinline__ uint64_t desc_sw128(const uint8_t* p, uint32_t lbo) {
+  return (smem_desc(p, lbo, 1024) & ~((uint64_t)7 << 61)) | (uint64_t)2 << 61;
+}
+template <int NP>
+__device__ __forceinline__ uint64_t desc_k(const uint8_t* tile, int s) {  // columns along K
+  if constexpr (NP == 1) return desc_sw128(tile + (s / 4) * (TILE / 2) + (s % 4) * 32, 16);
+  return smem_desc(tile + s * 2048, 1024, 128);
+}
+template <int NP>
+__device__ __forceinline__ uint64_t desc_mn(const uint8_t* tile, int s) {  // rows along K
+  if constexpr (NP == 1) return desc_sw128(tile + s * 2048, TILE / 2);
+  return smem_desc(tile + s * 256, 128, 1024);
+}
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// 64 tokens of one head (zeros past the tensor's end, and for columns past the head's width).
+__device__ __forceinline__ void tma_load_tile(uint8_t* dst, const CUtensorMap* map, int head, int t0, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, TILE);
+  tma_load(dst, map, 0, head, t0, bar);
+  tma_load(dst + TILE / 2, map, 64, head, t0, bar);
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Two f32 values as n bf16 parts each, packed in pairs (low half: x0); the parts sum to the
 // value to 8 n bits.
 template <int n>
@@ -106,35 +152,26 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t* out) {
 }
 __device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-// Whether a pair of bf16 holds an infinity or a NaN (an exponent of all ones).
-__device__ __forceinline__ uint32_t non_finite(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
-
-// Tiles are kept as [column / 8][row][8 columns]: 8 rows x 16 bytes are one core matrix, so the
+// Tiles written by threads are kept as [column / 8][row][8 columns]: 8 rows x 16 bytes are one core matrix, so the
 // same bytes serve as a K-major operand (columns along K: core matrices 1024 bytes apart
 // along K, 128 along rows) and as an MN-major one (rows along K: 128 along K, 1024 along columns).
 __device__ __forceinline__ uint32_t piece(int kc, int row) { return (uint32_t)(kc * CH + row) * 16u; }
 
-// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] matrix: four
-// 8-column pieces of one row. A warp's 32 pieces of one i are 64 contiguous bytes (16-bit
-// types) of 8 rows and fill four whole 128-byte lines of shared memory. One bf16 part goes
-// to shared memory as it is, asynchronously; other types pass through registers (fetch early,
-// put when the tile is free).
+// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] matrix that
+// needs several parts: four 8-column pieces of one row, fetched early and put into the tile
+// when that is free. A warp's 32 pieces of one i fill four whole 128-byte lines.
 template <typename T, int NP>
 struct Loader {
-  static constexpr int W = NP == 1 ? 1 : sizeof(T) * 2;  // 32-bit words of a piece held here
-  uint32_t r[D / 32][W];
-  __device__ __forceinline__ void fetch(uint8_t* dst, const T* src, int64_t stride, int t0, int n, int dim) {
-    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+  static constexpr int W = NP == 1 ? 4 : sizeof(T) * 2;  // 32-bit words of a piece
+  uint32_t r[NP == 1 ? 1 : D / 32][W];
+  __device__ __forceinline__ void fetch(const T* src, int64_t stride, int t0, int n, int dim) {
+    if constexpr (NP > 1) {
+      const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int kc = i * 4 + (lane >> 3);
-      const bool in = row < n && kc * 8 < dim;
-      const T* p = in ? src + (t0 + row) * stride + kc * 8 : src;
-      if constexpr (NP == 1) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst + piece(kc, row))), "l"(p),
-                     "r"(in ? 16 : 0)
-                     : "memory");
-      } else {
+      for (int i = 0; i < D / 32; ++i) {
+        const int kc = i * 4 + (lane >> 3);
+        const bool in = row < n && kc * 8 < dim;
+        const T* p = in ? src + (t0 + row) * stride + kc * 8 : src;
 #pragma unroll
         for (int j = 0; j < W / 4; ++j) {
           const uint4 u = in ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
@@ -167,11 +204,12 @@ struct Loader {
     }
   }
 };
-template <int pending>
-__device__ __forceinline__ void copies_wait() {  // all but the last `pending` groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(pending) : "memory");
+// Where piece kc (8 columns) of a row of a loaded tile is.
+template <int NP>
+__device__ __forceinline__ uint32_t tile_piece(int kc, int row) {
+  if constexpr (NP == 1) return (uint32_t)((kc >> 3) * (TILE / 2) + row * 128 + (((kc & 7) ^ (row & 7)) << 4));
+  return piece(kc, row);
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Eight values of a piece, the parts added up (exact: they do not overlap).
 template <int NP>
 __device__ __forceinline__ void read_piece(const uint8_t* p, float (&x)[8]) {
@@ -250,6 +288,8 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
   if (lane == 0) ph = 0.f, pl = 0.f, pr = 0;
   add(ph, pl, hi[0], lo[0]);
   pr += r[0];
+  const bool ok = fminf(ph, ch) > -80.f && fmaxf(ph, ch) < 20.f && ph == ph && ch == ch;
+  const bool mild = __all_sync(0xffffffffu, ok) && er == 0;
   const float gh[2] = {ph, ch}, gl[2] = {pl, cl};
   const int gr[2] = {pr, cr};
 #pragma unroll
@@ -258,26 +298,40 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
     m->g[t] = make_float4(gh[j], gl[j], (float)gr[j], expf(raw[j]));
     m->w[t] = gr[j] == er ? ex2((eh - gh[j]) + (el - gl[j])) : 0.f;
     m->eg[t] = gr[j] == 0 ? ex2(gh[j] + gl[j]) : 0.f;
+    m->ieg[t] = ex2(-(gh[j] + gl[j]));
   }
   if (lane == 0) {
     m->lam = er == 0 ? ex2(eh + el) : 0.f;
     m->ghi = eh;
     m->glo = el;
     m->reset = er != 0;
+    m->mild = mild;
   }
 }
+
+struct Maps {
+  CUtensorMap q, k, v, o;  // bf16 only
+};
 
 // MODE 0: the state that a unit's tokens alone leave, and its decay, into the workspace.
 // MODE 1: the outputs, from the state before the unit; the sequence's last unit stores it.
 // `wd`: decays [states][H], `wst`: states [states][H][dk][dv]; seg: tokens of a unit.
+//
+// Eight warps; thread 96 (warp 3, which has no scores to mask) also issues the products and
+// the TMA copies, each as soon as its inputs are ready and its target is free:
+//   QK | QS, KV while the scores are masked | PV; the next k after QK, q after QS, v after
+//   the outputs, which are turned in v's place, have left it.
+// Two bf16 CTAs share an SM, so one's products run beside the other's arithmetic.
 template <typename T, int NP, int MODE>
 __global__ void __launch_bounds__(256, NP == 1 ? 2 : 1)
-lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
+lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
   using L = Plan<NP>;
   constexpr int NPP = L::NPP, LIM = NP == 3 ? 2 : 1;  // products of parts i, j with i + j <= LIM
-  extern __shared__ __align__(1024) uint8_t sm[];
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, quarter = warp & 3;
+  const bool issuer = tid == 96;
   const int h = blockIdx.y, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
   pdl_wait_prior_grids();
   const Unit un = find_unit(a, seg, n_ws, blockIdx.x, m->scratch);
@@ -297,19 +351,40 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
   }
   if (warp == 0) tmem_alloc(&m->tmem, L::T_COLS);
   if (tid == 0) {
-    mbar_init(&m->bar, 1);
+    mbar_init(&m->full_q, 1);
+    mbar_init(&m->full_k, 1);
+    mbar_init(&m->full_v, 1);
+    mbar_init(&m->qk, 1);
+    mbar_init(&m->qs, 1);
+    mbar_init(&m->end, 1);
     fence_mbar_init();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = m->tmem, tlane = tm + ((uint32_t)quarter * 32u << 16);
-  const T* q = static_cast<const T*>(a.q) + (int64_t)(h / a.rep) * a.dk;
-  const T* k = static_cast<const T*>(a.k) + (int64_t)(h / a.rep) * a.dk;
+  const int hq = h / a.rep;
+  const T* q = static_cast<const T*>(a.q) + (int64_t)hq * a.dk;
+  const T* k = static_cast<const T*>(a.k) + (int64_t)hq * a.dk;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
   const int64_t sz = (int64_t)a.dk * a.dv;
   float* pool = a.state + ((int64_t)slot * a.H + h) * sz;
   float* mine = wst + ((int64_t)(un.slot0 + un.i) * a.H + h) * sz;  // sequences of several units
+
+  if (NP == 1 && issuer && begin < end) {
+    tma_load_tile(sm + L::K, &maps.k, hq, begin, &m->full_k);
+    if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, hq, begin, &m->full_q);
+    tma_load_tile(sm + L::V, &maps.v, h, begin, &m->full_v);
+  }
+  Loader<T, NP> lq, lk, lv;
+  if (NP > 1 && begin < end) {
+    const int n = min(CH, end - begin);
+    if (MODE == 1) lq.fetch(q, a.qs, begin, n, a.dk);
+    lk.fetch(k, a.ks, begin, n, a.dk);
+    if (MODE == 1) lq.put(sm + L::Q);
+    lk.put(sm + L::K);
+  }
+  if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
 
   // S^T: this thread's row, key columns 64 wg .. 64 wg + 63
   float S[64];
@@ -332,32 +407,11 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
         for (int p = 0; p < NPP; ++p) u[p][j] = s[p];
       }
 #pragma unroll
-      for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + p * 64 + wg * 32 + c * 16, u[p]);
+      for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + (wg * NPP + p) * 32 + c * 16, u[p]);
     }
     tmem_st_wait();
-    tc_fence_before_sync();
   };
-  if (MODE == 1) put_state();
-
-  uint32_t phase = 0;
-  bool ok = true;
-  float sum_hi = 0.f, sum_lo = 0.f;
-  int resets = 0;
-  Loader<T, NP> lq, lk, lv;
-  auto fetch_qk = [&](int t0) {
-    const int n = min(CH, end - t0);
-    if (t0 < end) {
-      if (MODE == 1) lq.fetch(sm + L::Q, q, a.qs, t0, n, a.dk);
-      lk.fetch(sm + L::K, k, a.ks, t0, n, a.dk);
-    }
-    copies_commit();
-  };
-  auto put_qk = [&]() {
-    if (MODE == 1) lq.put(sm + L::Q);
-    lk.put(sm + L::K);
-  };
-  // the state before the products that read it, and the state after the chunk's share
-  auto add_state = [&](float lam) {
+  auto add_state = [&](float lam) {  // S = lam S + A
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t r[16];
@@ -368,7 +422,8 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
     }
   };
   // A masked product with an infinity or a NaN is a NaN, which would reach the chunk's earlier
-  // tokens: a chunk whose v holds one goes token by token, from global memory.
+  // tokens: a chunk with such an output goes token by token, from global memory and the state
+  // before it.
   auto token_by_token = [&](int t0, int n, const Decays* d) {
     float* part = reinterpret_cast<float*>(sm + L::V);
     for (int t = 0; t < n; ++t) {
@@ -379,8 +434,7 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
       for (int c = 0; c < 16; ++c) {
         const int at = wg * 64 + c * 4;
         if (at < a.dk) {
-          const float4 kk = load4(k + (t0 + t) * a.ks + at);
-          const float4 qq = MODE == 1 ? load4(q + (t0 + t) * a.qs + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 kk = load4(k + (t0 + t) * a.ks + at), qq = load4(q + (t0 + t) * a.qs + at);
           const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, q4[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -389,37 +443,65 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
           }
         }
       }
-      if (MODE == 1) {
-        if (wg == 1) part[row] = acc;
-        __syncthreads();
-        if (wg == 0 && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>((acc + part[row]) * a.scale);
-        __syncthreads();
-      }
+      if (wg == 1) part[row] = acc;
+      __syncthreads();
+      if (wg == 0 && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>((acc + part[row]) * a.scale);
+      __syncthreads();
     }
+    fence_proxy_async_smem();
+    __syncthreads();
   };
-  auto v_non_finite = [&](const uint8_t* tile) {  // among this thread's own pieces
-    uint32_t bad = 0;
+  if (MODE == 1) put_state();
+
+  uint32_t ph = 0;  // parity of this chunk's phases
+  bool ok = true;
+  float sum_hi = 0.f, sum_lo = 0.f;
+  int resets = 0;
+  for (int t0 = begin; t0 < end; t0 += CH, ph ^= 1) {
+    const int n = min(CH, end - t0);
+    const Decays* d = &m->d[ph];
+    const bool more = t0 + CH < end;
+    // the state pass has no q: v alternates between the two places
+    uint8_t* tv = sm + (NP == 1 && MODE == 0 && ph ? L::Q : L::V);
+    if (NP > 1) {
+      fence_proxy_async_smem();
+      __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
+      lv.fetch(v, a.vs, t0, n, a.dv);
+    }
+    // ---- scores ----------------------------------------------------------------------
+    if (MODE == 1 && issuer) {
+      if (NP == 1) ok = mbar_wait(&m->full_q, ph) && mbar_wait(&m->full_k, ph) && ok;
+      tc_fence_after_sync();
+      each_product<NP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+        mma_f16(tm + L::T_O1, desc_k<NP>(sm + L::Q + i * TILE, s), desc_k<NP>(sm + L::K + j * TILE, s),
+                idesc_bf16(128, CH, 0, 0), !first);
+      });
+      mma_commit(&m->qk);
+    }
+    __syncwarp();
+    // ---- the decayed keys, three parts ------------------------------------------------
+    if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
+    if (NP == 1 && t0 == begin) __syncthreads();  // the first decays
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(tile + piece(i * 4 + (lane >> 3), warp * 8 + (lane & 7)));
-      bad |= non_finite(u.x) | non_finite(u.y) | non_finite(u.z) | non_finite(u.w);
+      const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
+      const float w = d->w[r];
+      float x[8];
+      read_piece<NP>(sm + L::K + tile_piece<NP>(kc, r), x);
+      uint32_t u[4][3];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // rows past the chunk's tokens are other sequences' or none
+        split_pair<3>(r < n ? x[2 * j] * w : 0.f, r < n ? x[2 * j + 1] * w : 0.f, u[j]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<uint4*>(sm + L::KT + p * TILE + piece(kc, r)) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
     }
-    return bad != 0;
-  };
-
-  if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
-  fetch_qk(begin);
-  put_qk();
-  int buf = 0;
-  for (int t0 = begin; t0 < end && ok; t0 += CH, buf ^= 1) {
-    const int n = min(CH, end - t0);
-    const Decays* d = &m->d[buf];
-    copies_wait<0>();
-    fence_proxy_async_smem();
-    __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
-    tc_fence_after_sync();
-    lv.fetch(sm + L::V, v, a.vs, t0, n, a.dv);
-    copies_commit();
+    if (NP == 1 && n < CH) {
+      ok = mbar_wait(&m->full_v, ph) && ok;
+      for (int i = n * 16 + tid; i < CH * 16; i += 256)
+        *reinterpret_cast<uint4*>(tv + tile_piece<1>(i & 15, i >> 4)) = make_uint4(0, 0, 0, 0);
+    }
+    lv.put(tv);
     sum_lo += d->glo;
     {
       const float s = sum_hi + d->ghi, bb = s - sum_hi;
@@ -427,65 +509,85 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
       sum_hi = s;
     }
     resets |= d->reset;
-    // ---- scores and the state's share ----------------------------------------------
-    if (MODE == 1 && tid == 0) {
-      each_product<NP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
-        mma_f16(tm + L::T_O1, smem_desc(sm + L::Q + i * TILE + s * 2048, 1024, 128),
-                smem_desc(sm + L::K + j * TILE + s * 2048, 1024, 128), idesc_bf16(128, CH, 0, 0), !first);
-      });
-      each_product<NPP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
-        mma_ts(tm + L::T_O2, tm + L::T_S + i * 64 + s * 8, smem_desc(sm + L::Q + j * TILE + s * 2048, 1024, 128),
-               idesc_bf16(128, CH, 0, 0), !first);
-      });
-      mma_commit(&m->bar);
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    if (__syncthreads_or(!ok)) {  // k has been read, the state's parts and the decayed keys are there
+      ok = false;
+      break;
     }
-    // the decayed keys, three parts
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int r = warp * 8 + (lane & 7);
-      const uint32_t at = piece(i * 4 + (lane >> 3), r);
-      const float w = d->w[r];
-      float x[8];
-      read_piece<NP>(sm + L::K + at, x);
-      uint32_t u[4][3];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) split_pair<3>(x[2 * j] * w, x[2 * j + 1] * w, u[j]);
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        *reinterpret_cast<uint4*>(sm + L::KT + p * TILE + at) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+    tc_fence_after_sync();
+    if (NP > 1 && more) {
+      const int n1 = min(CH, end - t0 - CH);
+      if (MODE == 1) lq.fetch(q, a.qs, t0 + CH, n1, a.dk);
+      lk.fetch(k, a.ks, t0 + CH, n1, a.dk);
     }
-    if (MODE == 1) {
-      ok = mbar_wait(&m->bar, phase);
-      phase ^= 1;
+    if (warp == 7 && more) chunk_decays(a, h, t0 + CH, min(CH, end - t0 - CH), &m->d[ph ^ 1]);
+    // ---- the state's share, and what the chunk adds to the state -------------------------
+    if (issuer) {
+      if (MODE == 1) {
+        each_product<NPP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+          mma_ts(tm + L::T_O2, tm + L::T_S + (s / 4 * NPP + i) * 32 + s % 4 * 8, desc_k<NP>(sm + L::Q + j * TILE, s),
+                 idesc_bf16(128, CH, 0, 0), !first);
+        });
+        mma_commit(&m->qs);
+        ok = mbar_wait(&m->qk, ph) && ok;
+      }
+      if (NP == 1 && more) tma_load_tile(sm + L::K, &maps.k, hq, t0 + CH, &m->full_k);
+      if (MODE == 1) ok = mbar_wait(&m->qs, ph) && ok;
+      if (NP == 1) ok = mbar_wait(&m->full_v, ph) && ok;
       tc_fence_after_sync();
+      each_product<NP, 3, 2, CH / 16>([&](int i, int j, int s, bool first) {
+        mma_f16(tm + L::T_A, desc_mn<NP>(tv + i * TILE, s), smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024),
+                idesc_bf16(128, D, 1, 1), !first);
+      });
+      if (NP == 1 && more) {
+        if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, hq, t0 + CH, &m->full_q);
+        else tma_load_tile(sm + (ph ? L::V : L::Q), &maps.v, h, t0 + CH, &m->full_v);
+      }
+      if (MODE == 0) mma_commit(&m->end);
     }
-    __syncthreads();  // q and k have been read: the next chunk's may come
-    fetch_qk(t0 + CH);
-    if (warp == 7 && t0 + CH < end) chunk_decays(a, h, t0 + CH, min(CH, end - t0 - CH), &m->d[buf ^ 1]);
+    __syncwarp();
+    // ---- masked scores and the chunk's own share -----------------------------------------
     if (MODE == 1 && quarter < 2 && wg <= quarter) {
       // Lanes 0 .. 63 hold the tokens' rows of scores; columns 32 wg .. 32 wg + 31 here, of
       // which the mask leaves none for rows below 32 and wg 1.
+      ok = mbar_wait(&m->qk, ph) && ok;
+      tc_fence_after_sync();
       const float4 gt = d->g[row];
+      const float et = d->eg[row];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int step = wg * 2 + c;  // of the product over s
         uint32_t s[16];
         tmem_ld16(tlane + L::T_O1 + step * 16, s);
         tmem_ld_wait();
+        // exp(G_t - G_s): where the chunk's decays are mild, as a product of two factors (16-bit
+        // types; a score that overflows on the way ends in the token-by-token form)
+        if (NP < 3 && d->mild) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = *reinterpret_cast<const float4*>(&d->ieg[step * 16 + 4 * j]);
+            s[4 * j] = __float_as_uint(__uint_as_float(s[4 * j]) * f.x * et);
+            s[4 * j + 1] = __float_as_uint(__uint_as_float(s[4 * j + 1]) * f.y * et);
+            s[4 * j + 2] = __float_as_uint(__uint_as_float(s[4 * j + 2]) * f.z * et);
+            s[4 * j + 3] = __float_as_uint(__uint_as_float(s[4 * j + 3]) * f.w * et);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 gs = d->g[step * 16 + j];
+            const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
+            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * x) : 0u;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t u[4][NPP];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float p[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int col = step * 16 + e * 8 + 2 * j + f;
-              const float4 gs = d->g[col];
-              const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
-              p[f] = col <= row && gt.z == gs.z ? __uint_as_float(s[e * 8 + 2 * j + f]) * x : 0.f;
-            }
-            split_pair<NPP>(p[0], p[1], u[j]);
+            const int c0 = e * 8 + 2 * j;
+            split_pair<NPP>(step * 16 + c0 <= row ? __uint_as_float(s[c0]) : 0.f,
+                            step * 16 + c0 + 1 <= row ? __uint_as_float(s[c0 + 1]) : 0.f, u[j]);
           }
           if (row >= step * 16) {
 #pragma unroll
@@ -495,71 +597,96 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
           }
         }
       }
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      asm volatile("bar.arrive 1, 128;" ::: "memory");  // three warps of scores and the issuer's
     }
-    lv.put(sm + L::V);
-    copies_wait<1>();
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    if (__syncthreads_or(v_non_finite(sm + L::V))) {
-      token_by_token(t0, n, d);
-      put_qk();
-      if (MODE == 1) put_state();
-      ok = !__syncthreads_or(!ok);
-      continue;
-    }
-    tc_fence_after_sync();
-    // ---- the chunk's own share, and what it adds to the state ------------------------------
-    if (tid == 0) {
-      if (MODE == 1)
+    if (MODE == 1 && warp == 3) {
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      tc_fence_after_sync();
+      if (issuer) {
         each_product<NP, NPP, LIM, CH / 16>([&](int i, int j, int s, bool first) {
-          mma_f16(tm + L::T_O1 + s * 16, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
+          mma_f16(tm + L::T_O1 + s * 16, desc_mn<NP>(tv + i * TILE, s),
                   smem_desc(sm + L::P + j * PTILE + p_base(s), p_pitch(s), 128), idesc_bf16(128, CH - 16 * s, 1, 0),
                   !first);
         });
-      each_product<NP, 3, 2, CH / 16>([&](int i, int j, int s, bool first) {
-        mma_f16(tm + L::T_A, smem_desc(sm + L::V + i * TILE + s * 256, 128, 1024),
-                smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024), idesc_bf16(128, D, 1, 1), !first);
-      });
-      mma_commit(&m->bar);
+        mma_commit(&m->end);
+      }
+      __syncwarp();
     }
-    ok = mbar_wait(&m->bar, phase) && ok;
-    phase ^= 1;
+    ok = mbar_wait(&m->end, ph) && ok;
     tc_fence_after_sync();
-    add_state(d->lam);
-    if (MODE == 1) {
-      // outputs, a thread's row is one value channel: turned in v's place into rows of tokens
-      T* stage = reinterpret_cast<T*>(sm + L::V);
+    if (MODE == 0) {
+      add_state(d->lam);
+      lk.put(sm + L::K);
+      if (NP == 1) __syncthreads();  // the next decays are there
+      continue;
+    }
+    // ---- outputs ----------------------------------------------------------------------
+    // A thread's row is one value channel: turned in v's place into rows of tokens, whole
+    // ones for 32-bit types, two halves of 64 channels otherwise.
+    T* stage = reinterpret_cast<T*>(sm + L::V);
+    constexpr int SW = sizeof(T) == 4 ? D : 64;  // channels of a staged row
+    float bad = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o1[16], o2[16];
-        tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, o1);
-        tmem_ld16(tlane + L::T_O2 + wg * 32 + c * 16, o2);
-        tmem_ld_wait();
+    for (int c = 0; c < 2; ++c) {
+      uint32_t o1[16], o2[16];
+      tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, o1);
+      tmem_ld16(tlane + L::T_O2 + wg * 32 + c * 16, o2);
+      tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = wg * 32 + c * 16 + j;
-          const float x = fmaf(d->eg[t], __uint_as_float(o2[j]), __uint_as_float(o1[j]));
-          stage[t * D + row] = from_f32<T>(x * a.scale);
+      for (int j = 0; j < 16; j += 4) {
+        const int t = wg * 32 + c * 16 + j;
+        const float4 e = *reinterpret_cast<const float4*>(&d->eg[t]);
+        const float ev[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float x = fmaf(ev[f], __uint_as_float(o2[j + f]), __uint_as_float(o1[j + f])) * a.scale;
+          if (t + f < n) bad = fmaf(x, 0.f, bad);
+          stage[(row / SW) * CH * SW + (t + f) * SW + row % SW] = from_f32<T>(x);
         }
       }
     }
-    put_qk();
+    lq.put(sm + L::Q);
+    lk.put(sm + L::K);
+    fence_proxy_async_smem();
     tc_fence_before_sync();
-    ok = !__syncthreads_or(!ok);
+    const bool redo = __syncthreads_or(bad != 0.f);  // a sum of zeros unless a value is not finite
     tc_fence_after_sync();
-    if (MODE == 1) {
-      put_state();
-      constexpr int PC = D * (int)sizeof(T) / 16;  // 16-byte pieces of a token's row
-#pragma unroll
-      for (int i = 0; i < CH * PC / 256; ++i) {
-        const int t = (i * 256 + tid) / PC, c = (i * 256 + tid) % PC;
-        if (t < n && c * (16 / (int)sizeof(T)) < a.dv)
-          *reinterpret_cast<uint4*>(o + (t0 + t) * a.os + c * (16 / sizeof(T))) =
-              *reinterpret_cast<const uint4*>(sm + L::V + (i * 256 + tid) * 16);
+    if (redo) {
+      token_by_token(t0, n, d);
+    } else {
+      if (NP == 1 && n == CH) {
+        if (issuer) {
+          tma_store(&maps.o, stage, 0, h, t0);
+          if (a.dv > 64) tma_store(&maps.o, stage + CH * SW, 64, h, t0);
+          store_commit();
+        }
+      } else {
+        constexpr int PC = SW * (int)sizeof(T) / 16;  // 16-byte pieces of a staged row
+        for (int i = tid; i < CH * (D / SW) * PC; i += 256) {
+          const int t = i / PC % CH, c = i / PC / CH * SW + i % PC * (16 / (int)sizeof(T));
+          if (t < n && c < a.dv)
+            *reinterpret_cast<uint4*>(o + (t0 + t) * a.os + c) =
+                *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(stage) + i * 16);
+        }
       }
+      add_state(d->lam);
     }
+    put_state();
+    if (NP == 1 && issuer) {
+      store_wait_read();
+      if (more) tma_load_tile(sm + L::V, &maps.v, h, t0 + CH, &m->full_v);
+    }
+    __syncwarp();
   }
-  copies_wait<0>();
+  if (NP == 1 && issuer && begin < end) {  // no copy is left in flight, whatever ended the loop
+    const uint32_t p = ok ? ph ^ 1 : ph;
+    ok = mbar_wait(&m->full_k, p) && ok;
+    if (MODE == 1) ok = mbar_wait(&m->full_q, p) && ok;
+    ok = mbar_wait(&m->full_v, p) && ok;
+  }
+  ok = !__syncthreads_or(!ok);
   if (!ok && tid == 0) atomicOr(ctrl + CTRL_STATUS, DEV_ERR_MBAR_TIMEOUT);
   float* to = MODE == 0 ? mine + (int64_t)a.H * sz : pool;  // what a unit leaves is the next one's start
   if (ok && (MODE == 0 || end == last)) {
@@ -568,6 +695,7 @@ lin_chunk(LinattnArgs a, int seg, int n_ws, float* wd, float* wst, uint32_t* ctr
       if (row < a.dv && wg * 64 + j < a.dk) to[(wg * 64 + j) * a.dv + row] = S[j];
   }
   if (MODE == 0 && tid == 0) wd[(int64_t)(un.slot0 + un.i) * a.H + h] = resets ? 0.f : ex2(sum_hi + sum_lo);
+  if (NP == 1 && MODE == 1 && issuer) store_wait_all();
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tm, L::T_COLS);
@@ -615,23 +743,54 @@ cudaError_t launch(K kern, dim3 grid, int smem, bool pdl, cudaStream_t st, Args.
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// A [tokens][heads][dim] bf16 tensor in boxes of 64 tokens x 64 columns of one head, rows of
+// 128 bytes, in the 128-byte swizzle for operands and as they are for outputs.
+cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int tokens, int64_t stride, bool swizzle) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r{};
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+    if (e != cudaSuccess) return e;
+    if (r != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename T, int NP>
 cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream_t st) {
   const LinattnSplit sp = linattn_split(a.N, a.B, a.H, a.dk, a.dv);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws);
   float* wd = reinterpret_cast<float*>(ws + sp.decays);
   float* wst = reinterpret_cast<float*>(ws + sp.states);
-  const dim3 grid((unsigned)sp.units, (unsigned)a.H);
-  const bool several = a.offsets ? sp.units > a.B : a.seq_len > sp.seg;
+  Maps maps{};
   cudaError_t e = cudaSuccess;
+  if (NP == 1 && a.N > 0) {
+    const int G = a.H / a.rep;
+    if ((e = make_map(&maps.q, a.q, a.dk, G, a.N, a.qs, true)) != cudaSuccess) return e;
+    if ((e = make_map(&maps.k, a.k, a.dk, G, a.N, a.ks, true)) != cudaSuccess) return e;
+    if ((e = make_map(&maps.v, a.v, a.dv, a.H, a.N, a.vs, true)) != cudaSuccess) return e;
+    if ((e = make_map(&maps.o, a.o, a.dv, a.H, a.N, a.os, false)) != cudaSuccess) return e;
+  }
+  const dim3 grid((unsigned)sp.units, (unsigned)a.H);
+  const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
+  const bool several = a.offsets ? sp.units > a.B : a.seq_len > sp.seg;
   if (several) {
-    e = launch(lin_chunk<T, NP, 0>, grid, Plan<NP>::BYTES, pdl, st, a, sp.seg, sp.n_ws, wd, wst, ctrl);
+    e = launch(lin_chunk<T, NP, 0>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
     if (e != cudaSuccess) return e;
     const dim3 jgrid((unsigned)sp.units, (unsigned)a.H, (unsigned)((a.dk * a.dv + 1023) / 1024));
     e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1>, grid, Plan<NP>::BYTES, pdl, st, a, sp.seg, sp.n_ws, wd, wst, ctrl);
+  return launch(lin_chunk<T, NP, 1>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
 }
 
 }  // namespace
