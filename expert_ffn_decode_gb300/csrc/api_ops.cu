@@ -50,7 +50,8 @@ int check_matvec(const moe_matvec_cfg* c) {
   if (c->rows < 1) return set_error(MOE_ERR_INVALID_CFG, "rows %d: must be positive", c->rows);
   if (c->cols < 32 || c->cols > 16384 || c->cols % unit)
     return set_error(MOE_ERR_INVALID_CFG, "cols %d: must be a multiple of %d, at most 16384", c->cols, unit);
-  if (c->n_vec < 0) return set_error(MOE_ERR_INVALID_CFG, "n_vec %d < 0", c->n_vec);
+  if (c->n_vec < 0 || c->n_vec > 65535)
+    return set_error(MOE_ERR_INVALID_CFG, "n_vec %d: must be in [0, 65535]", c->n_vec);
   if (!type_bytes(c->x_type) || !type_bytes(c->y_type))
     return set_error(MOE_ERR_INVALID_CFG, "x_type %d, y_type %d: expected MOE_F32, MOE_F16 or MOE_BF16", c->x_type,
                      c->y_type);

@@ -3,7 +3,27 @@
 // A row's block of 32 values with scale d and offset m contributes
 //   d * sum_i q_i x_i + m * sum_i x_i
 // (Q4_0 and planes without offsets: m = -8 d; Q4_K: d and m are the sub-block's d sc and
-// -dmin mn), so a nibble is used as the integer it is and never rounded.
+// -dmin mn), so a nibble is used as the integer it is and never rounded. The inner sum runs on
+// the tensor cores by mma.m16n8k16, whose operands are registers: at one vector there is a
+// matrix row of work for one accumulator column, far too little for a tcgen05 tile, and the
+// kernel is bound by the weights' bytes. What mma buys is instructions: a pair of nibbles
+// becomes an f16 operand by one AND (the bits of a nibble in the low bits of an f16 are the
+// subnormal q 2^-24, or 16 q 2^-24 for the high one) and one multiplication by a power of two
+// to q 2^-10; about 1.8 instructions a weight, where an f32 dot takes 2.4. The multiplication is
+// needed for the sums, not for the values: a subnormal operand counts in the accumulator's
+// alignment with the exponent of the smallest normal number, and up to ten bits of every
+// product are lost (1.2 times outside the rounding bound beside a value 10^6 times its
+// neighbours).
+//
+// x is held as f16 pieces: within a block of 32 values it is scaled by a power of two that
+// puts the largest magnitude at 2^13 .. 2^14, then split into two parts (22 bits of each value;
+// 16-bit types in calls of several vectors take one, which holds them). Sums are f32. (A 24-bit
+// fixed point of the block was 1.3 times outside the bound in the same place.)
+//
+// Columns of one mma are (vector, part) pairs. A single vector has two of eight: the other six
+// take three more blocks. Lane t of a quad of lanes then holds a whole block's nibbles of its
+// row, and x is zero outside the columns of the lane's own block, so the accumulator's
+// column pair t is block t's sum and each lane applies one block's scale.
 #include "common.cuh"
 #include "ops_host.h"
 #include "types.cuh"
@@ -11,77 +31,504 @@
 namespace moe {
 namespace {
 
-// One warp a row, a lane every 32nd block.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(256) matvec_kernel(MatvecArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int nb = a.cols / 32;
-  if (row >= a.rows) return;
-  for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
-    const TX* x = static_cast<const TX*>(a.x) + t * a.xs;
-    float acc = 0.f;
-    for (int b = lane; b < nb; b += 32) {
-      const uint8_t* nib;
-      int nib_shift = -1;  // Q4_K: a sub-block is one nibble of 32 bytes
-      float d, m;
-      if (a.qtype == MOE_Q4_K) {
-        const uint8_t* s = a.w + (row * (nb / 8) + b / 8) * 144;
-        const int j = b % 8;
-        const uint8_t* p = s + 4;
-        const int sc = j < 4 ? p[j] & 63 : (p[j + 4] & 15) | (p[j - 4] >> 6) << 4;
-        const int mn = j < 4 ? p[j + 4] & 63 : (p[j + 4] >> 4) | (p[j] >> 6) << 4;
-        d = __half2float(*reinterpret_cast<const __half*>(s)) * sc;
-        m = -__half2float(*reinterpret_cast<const __half*>(s + 2)) * mn;
-        nib = s + 16 + j / 2 * 32;
-        nib_shift = j % 2 * 4;
-      } else if (a.qtype == MOE_Q4_PLANES) {
-        nib = a.w + (row * nb + b) * 16;
-        const int64_t g = row * (a.cols / a.group) + b * 32 / a.group;
-        d = __half2float(reinterpret_cast<const __half*>(a.scales)[g]);
-        m = a.mins ? __half2float(reinterpret_cast<const __half*>(a.mins)[g]) : -8.f * d;
-      } else {
-        const bool q1 = a.qtype == MOE_Q4_1;
-        const uint8_t* s = a.w + (row * nb + b) * (q1 ? 20 : 18);
-        d = __half2float(*reinterpret_cast<const __half*>(s));
-        m = q1 ? __half2float(*reinterpret_cast<const __half*>(s + 2)) : -8.f * d;
-        nib = s + (q1 ? 4 : 2);
-      }
-      float s = 0.f, sx = 0.f;
-      for (int i = 0; i < 32; ++i) {
-        const float xv = to_f32(x[b * 32 + i]);
-        const int q = nib_shift >= 0 ? nib[i] >> nib_shift & 15 : nib[i % 16] >> i / 16 * 4 & 15;
-        s = fmaf((float)q, xv, s);
-        sx += xv;
-      }
-      acc = fmaf(d, s, acc);
-      acc = fmaf(m, sx, acc);
+constexpr int MV_WARPS = 8;
+constexpr int MV_DEPTH = 4;      // stages of a warp's ring: three in flight
+constexpr int MV_PITCH = 176;    // bytes of a staged row: 256 values of the widest type and 16 of misalignment;
+                                 // 48 mod 128 spreads four 20-byte blocks of 8 rows over all banks
+constexpr int MV_SPITCH = 32;    // planes: staged bytes of a row's scales (and of its offsets)
+
+// Types of weight rows, as template values.
+enum { ROW_Q4_0, ROW_Q4_1, ROW_Q4_K, ROW_PLANES };
+
+// How a call's vectors sit in the mma columns.
+//   MULTI false: one vector, four blocks an mma.
+//   MULTI true: NT tiles of 8 columns of PARTS parts, one block an mma.
+template <bool MULTI_, int NT_, int PARTS_>
+struct Cols {
+  static constexpr bool MULTI = MULTI_;
+  static constexpr int NT = NT_, PARTS = PARTS_;
+  static constexpr int VECS = MULTI ? 8 * NT / PARTS : 1;
+  static constexpr int XBYTES = MULTI ? 16 * NT : 4;  // bytes of x pieces for each of a row's values
+};
+
+struct MvArgs {
+  MatvecArgs a;
+  int64_t row_bytes, total;    // of the weights (planes: of the nibble plane)
+  int64_t srow, stotal;        // planes: of the scales and of the offsets
+  int nb;                      // blocks of a row
+  int nq;                      // runs of 128 values of a row (the last may be partial)
+  int unit;                    // runs that one warp takes whole: 2 for Q4_K (a super-block)
+  int ks;                      // warps that share a tile of 16 rows
+  int tiles;
+  int pdl;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The nibbles of word w (rows g) and u (rows g + 8) against x pieces: low nibbles are values
+// 4 j .. 4 j + 3 of a half block in the order 0, 2 | 1, 3, high ones of the other half.
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t low_h2(uint32_t w) { return mul_h2(w & 0x000f000fu, 0x74007400u); }   // 2^14
+__device__ __forceinline__ uint32_t high_h2(uint32_t w) { return mul_h2(w & 0x00f000f0u, 0x64006400u); }  // 2^10
+__device__ __forceinline__ void mma_low(float (&c)[4], uint32_t w, uint32_t u, uint32_t b0, uint32_t b1) {
+  mma16816(c, low_h2(w), low_h2(u), low_h2(w >> 8), low_h2(u >> 8), b0, b1);
+}
+__device__ __forceinline__ void mma_high(float (&c)[4], uint32_t w, uint32_t u, uint32_t b0, uint32_t b1) {
+  mma16816(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
+}
+__device__ __forceinline__ float half_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// x in f16 pieces, and for each block and vector {2^10 / scale, sum of x}. A thread takes four
+// values of a vector; the eight threads of a block are neighbours. Values past the row's end
+// are not written: they belong to blocks whose sums are dropped.
+template <int RT, class C, typename TX>
+__device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t* xf, float2* info) {
+  const TX* x = static_cast<const TX*>(p.a.x) + t0 * p.a.xs;
+  const int per = p.a.cols / 4;
+  for (int i = threadIdx.x; i < per * nv; i += MV_WARPS * 32) {  // a block's 8 threads stay together
+    const int vec = i / per, at = i % per * 4;
+    const float4 v = load4(x + vec * p.a.xs + at);
+    float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+    float sum = (v.x + v.y) + (v.z + v.w);
+    const unsigned group = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
+      sum += __shfl_xor_sync(group, sum, o);
     }
-    acc = warp_sum(acc);
-    if (lane == 0) {
-      if (a.bias) acc += a.bias[row];
-      TY* y = static_cast<TY*>(a.y) + t * a.ys + row;
-      if (a.flags & MOE_ACCUMULATE) acc += to_f32(*y);
-      *y = from_f32<TY>(acc);
+    // largest magnitude 2^e (1 .. 2): scale 2^(13 - e); it and 2^10 / it stay normal
+    const int e = min(max((int)(__float_as_uint(mx) >> 23), 27), 253);
+    const float sc = __uint_as_float((uint32_t)(267 - e) << 23);
+    const float back = __uint_as_float((uint32_t)(e - 13) << 23);  // 1 / sc
+    const int b = at / 32, r = at % 32;
+    const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
+    float hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = __half2float(__float2half_rn(f[j]));
+      lo[j] = f[j] - hi[j];
+    }
+    const uint2 parts[2] = {make_uint2(pack_h2(hi[0], hi[2]), pack_h2(hi[1], hi[3])),
+                            make_uint2(pack_h2(lo[0], lo[2]), pack_h2(lo[1], lo[3]))};
+    if constexpr (!C::MULTI) {
+      int quad, t, nib;
+      if (RT == ROW_Q4_K) {  // lane t: 16 bytes, half t % 2 of a run; nibble: which sub-block of the run
+        quad = b / 4;
+        t = (b >> 1 & 1) * 2 + r / 16;
+        nib = b & 1;
+      } else {
+        quad = b / 4;
+        t = b & 3;
+        nib = r / 16;
+      }
+      const int j = r % 16 / 4;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<uint2*>(xf + quad * 512 + (nib * 2 + j / 2) * 128 + (2 * t + q) * 16 + j % 2 * 8) = parts[q];
+      if ((threadIdx.x & 7) == 0) info[b] = make_float2(back * 1024.f, sum);
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::PARTS; ++q) {
+        const int n = vec * C::PARTS + q;
+        const int lane = n % 8 * 4 + r % 16 / 4;
+        *reinterpret_cast<uint2*>(xf + ((b * C::NT + n / 8) * 32 + lane) * 16 + r / 16 * 8) = parts[q];
+      }
+      if ((threadIdx.x & 7) == 0) info[b * C::VECS + vec] = make_float2(back * 1024.f, sum);
     }
   }
 }
 
-template <typename TX>
-cudaError_t launch_y(const MatvecArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.rows + 7) / 8), (unsigned)(a.T < 64 ? a.T : 64));
-  if (a.y_type == MOE_F32) matvec_kernel<TX, float><<<grid, 256, 0, st>>>(a);
-  else if (a.y_type == MOE_F16) matvec_kernel<TX, __half><<<grid, 256, 0, st>>>(a);
-  else matvec_kernel<TX, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+// The scale and offset of Q4_K sub-block j from its super-block's 16 header bytes.
+__device__ __forceinline__ void q4k_scale(uint4 h, int j, float& d, float& m) {
+  const uint32_t s = j & 3, sh = s * 8;
+  uint32_t sc, mn;
+  if (j < 4) {
+    sc = h.y >> sh & 63;
+    mn = h.z >> sh & 63;
+  } else {
+    const uint32_t b = h.w >> sh;
+    sc = (b & 15) | (h.y >> sh >> 6 & 3) << 4;
+    mn = (b >> 4 & 15) | (h.z >> sh >> 6 & 3) << 4;
+  }
+  d = half_bits(h.x & 0xffffu) * (float)sc;
+  m = -half_bits(h.x >> 16) * (float)mn;
+}
+
+__device__ __forceinline__ void copy16(void* dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// A warp's steps: the tiles of its group in turn, and in each its range of runs two at a time
+// (256 values). Each step's rows are copied to the warp's own ring, three steps ahead, so a
+// warp never waits for another one but to join the partial sums of a tile.
+template <int RT, class C>
+__global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_constant__ MvArgs p) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int STAGE = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = sm + warp * MV_DEPTH * STAGE;
+  uint8_t* xf = sm + MV_WARPS * MV_DEPTH * STAGE;
+  float2* info = reinterpret_cast<float2*>(xf + (size_t)(p.nq * 128) * C::XBYTES);
+  float* red = reinterpret_cast<float*>(info + p.nq * 4 * C::VECS);  // [2][warps][16 * VECS]
+  float4* zero = reinterpret_cast<float4*>(red + 2 * MV_WARPS * 16 * C::VECS);
+  const int groups = MV_WARPS / p.ks, group = warp / p.ks, part = warp % p.ks;
+  const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
+  const int units = (p.nq + p.unit - 1) / p.unit;
+  const int qa = units * part / p.ks * p.unit, qb = min(units * (part + 1) / p.ks * p.unit, p.nq);
+  const int per_tile = (qb - qa + 1) / 2;
+  const int my_tiles = first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
+  const int steps = my_tiles * per_tile;
+
+  if (p.pdl) pdl_launch_dependents();
+  // ---- weights: the copies of one step -----------------------------------------------
+  int c_tile = first, c_q = qa, c_step = 0;  // the next step to copy
+  const int crow = lane >> 1;                // two lanes a row, 32 bytes a turn
+  auto copy_step = [&]() {
+    if (c_step < steps) {
+      uint8_t* dst = ring + c_step % MV_DEPTH * STAGE;
+      const int64_t row = (int64_t)c_tile * 16 + crow;
+      if (row < p.a.rows) {
+        const int runs = min(2, qb - c_q), blocks = min(runs * 4, p.nb - c_q * 4);
+        const int64_t from = row * p.row_bytes +
+                             (RT == ROW_Q4_0 ? c_q * 72 : RT == ROW_Q4_1 ? c_q * 80 : RT == ROW_Q4_K ? c_q / 2 * 144 : c_q * 64);
+        const int bytes = RT == ROW_Q4_0 ? blocks * 18 : RT == ROW_Q4_1 ? blocks * 20 : RT == ROW_Q4_K ? 144 : blocks * 16;
+        const int64_t lo = from & ~(int64_t)15;
+        const int n = (int)(from + bytes - lo);  // bytes of the window up to the last one wanted
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          const int at = (2 * i + (lane & 1)) * 16;
+          // the last piece stops at the array's end
+          if (at < n) copy16(dst + crow * MV_PITCH + at, p.a.w + lo + at, (int)min((int64_t)16, p.total - lo - at));
+        }
+        if constexpr (RT == ROW_PLANES) {
+          const int64_t sf = (row * (p.a.cols / p.a.group) + c_q * 128 / p.a.group) * 2, sl = sf & ~(int64_t)15;
+          const int at = (lane & 1) * 16;
+          const int left = (int)min((int64_t)16, p.stotal - sl - at);
+          if (left > 0) {
+            copy16(dst + 16 * MV_PITCH + crow * MV_SPITCH + at, p.a.scales + sl + at, left);
+            if (p.a.mins) copy16(dst + 16 * (MV_PITCH + MV_SPITCH) + crow * MV_SPITCH + at, p.a.mins + sl + at, left);
+          }
+        }
+      }
+      ++c_step;
+      c_q += 2;
+      if (c_q >= qb) {
+        c_q = qa;
+        c_tile += stride;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < MV_DEPTH - 1; ++i) copy_step();
+
+  // ---- x ------------------------------------------------------------------------------
+  pdl_wait_prior_grids();
+  const int t0 = blockIdx.y * C::VECS, nv = min(C::VECS, p.a.T - t0);
+  if (p.a.x_type == MOE_F32) stage_x<RT, C, float>(p, t0, nv, xf, info);
+  else if (p.a.x_type == MOE_F16) stage_x<RT, C, __half>(p, t0, nv, xf, info);
+  else stage_x<RT, C, __nv_bfloat16>(p, t0, nv, xf, info);
+  if (tid == 0) *zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+
+  // single vector: where this lane's x pieces are, or a zero (column n = lane / 4 is part n & 1
+  // of the block, or sub-block, n / 2 of the run)
+  const uint8_t* xl[2];
+  int xstep[2];
+#pragma unroll
+  for (int nib = 0; nib < 2; ++nib) {
+    const int slot = RT == ROW_Q4_K ? (t & 2) + nib : t;
+    const bool mine = g >> 1 == slot;
+    xl[nib] = mine ? xf + nib * 256 + (2 * t + (g & 1)) * 16 : reinterpret_cast<const uint8_t*>(zero);
+    xstep[nib] = mine;
+  }
+
+  constexpr int AV = C::MULTI ? 2 / C::PARTS : 1;  // vectors of a lane in a tile of columns
+  float acc[C::NT][AV][2];                         // [column tile][vector][row g, g + 8]
+#pragma unroll
+  for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+    for (int v = 0; v < AV; ++v) acc[n][v][0] = acc[n][v][1] = 0.f;
+
+  int step = 0;
+  for (int k = 0, tile = first; k < my_tiles; ++k, tile += stride) {
+    for (int q0 = qa; q0 < qb; q0 += 2, ++step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(MV_DEPTH - 2) : "memory");
+      __syncwarp();
+      const uint8_t* st = ring + step % MV_DEPTH * STAGE;
+      // where the two rows' windows start in the stage, and their scales'
+      const uint8_t* base[2];
+      const uint8_t* sbase[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t row = (int64_t)tile * 16 + g + 8 * r;
+        int mis = 0;
+        if (RT == ROW_Q4_0) mis = (int)((row * p.row_bytes + q0 * 72) & 15);
+        if (RT == ROW_Q4_1) mis = (int)((row * p.row_bytes + q0 * 80) & 15);
+        base[r] = st + (g + 8 * r) * MV_PITCH + mis;
+        sbase[r] = st + 16 * MV_PITCH + (g + 8 * r) * MV_SPITCH;
+        if (RT == ROW_PLANES) sbase[r] += (int)((row * (p.a.cols / p.a.group) + q0 * 128 / p.a.group) * 2 & 15);
+      }
+      // word i of block b (of the step) of row r, and the block's scale and offset
+      auto scale_of = [&](int r, int b, float& d, float& m) {
+        if constexpr (RT == ROW_Q4_1) {
+          const uint32_t h = *reinterpret_cast<const uint32_t*>(base[r] + b * 20);
+          d = half_bits(h & 0xffffu);
+          m = half_bits(h >> 16);
+        } else if constexpr (RT == ROW_Q4_0) {
+          d = half_bits(*reinterpret_cast<const uint16_t*>(base[r] + b * 18));
+          m = -8.f * d;
+        } else if constexpr (RT == ROW_Q4_K) {
+          q4k_scale(*reinterpret_cast<const uint4*>(base[r]), b, d, m);
+        } else {
+          const int at = b * 32 / p.a.group * 2;
+          d = half_bits(*reinterpret_cast<const uint16_t*>(sbase[r] + at));
+          m = p.a.mins ? half_bits(*reinterpret_cast<const uint16_t*>(sbase[r] + 16 * MV_SPITCH + at)) : -8.f * d;
+        }
+      };
+#pragma unroll
+      for (int qq = 0; qq < 2; ++qq) {
+        const int quad = q0 + qq;
+        if (quad >= qb) break;
+        if constexpr (!C::MULTI) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(xl[i / 2] + (xstep[i / 2] ? quad * 512 + (i & 1) * 128 : 0));
+          const int b = qq * 4 + t;  // this lane's block of the step
+          uint32_t w[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if constexpr (RT == ROW_Q4_0) {
+              const uint8_t* s = base[r] + b * 18;
+              const uint32_t* u = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(s) & ~(uintptr_t)3);
+              const uint32_t sh = reinterpret_cast<uintptr_t>(s) & 2 ? 32 : 16;
+              uint32_t v[5];
+#pragma unroll
+              for (int i = 0; i < 5; ++i) v[i] = u[i];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[r][i] = __funnelshift_rc(v[i], v[i + 1], sh);
+            } else if constexpr (RT == ROW_Q4_1) {
+              const uint32_t* u = reinterpret_cast<const uint32_t*>(base[r] + b * 20 + 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[r][i] = u[i];
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(base[r] + (RT == ROW_Q4_K ? 16 : 0) + b * 16);
+              w[r][0] = u.x;
+              w[r][1] = u.y;
+              w[r][2] = u.z;
+              w[r][3] = u.w;
+            }
+          }
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_low(c, w[0][j], w[1][j], j & 1 ? x[j / 2].z : x[j / 2].x, j & 1 ? x[j / 2].w : x[j / 2].y);
+            mma_high(c, w[0][j], w[1][j], j & 1 ? x[2 + j / 2].z : x[2 + j / 2].x,
+                     j & 1 ? x[2 + j / 2].w : x[2 + j / 2].y);
+          }
+          if (quad * 4 + t < p.nb) {
+            const float2 in = info[quad * 4 + t];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float d, m;
+              scale_of(r, b, d, m);
+              acc[0][0][r] = fmaf(d * in.x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
+              acc[0][0][r] = fmaf(m, in.y, acc[0][0][r]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int b = qq * 4 + i, blk = quad * 4 + i;
+            if (blk >= p.nb) break;
+            uint32_t w0[2], w1[2];  // the words of the first and the second 16 values
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (RT == ROW_Q4_0) {
+                const uint8_t* s = base[r] + b * 18 + 2 + t * 4;
+                w0[r] = *reinterpret_cast<const uint16_t*>(s) | (uint32_t)*reinterpret_cast<const uint16_t*>(s + 2) << 16;
+              } else if constexpr (RT == ROW_Q4_1) {
+                w0[r] = *reinterpret_cast<const uint32_t*>(base[r] + b * 20 + 4 + t * 4);
+              } else if constexpr (RT == ROW_PLANES) {
+                w0[r] = *reinterpret_cast<const uint32_t*>(base[r] + b * 16 + t * 4);
+              } else {  // sub-block b: a nibble of the run's 32 bytes
+                w0[r] = *reinterpret_cast<const uint32_t*>(base[r] + 16 + b / 2 * 32 + t * 4);
+                w1[r] = *reinterpret_cast<const uint32_t*>(base[r] + 16 + b / 2 * 32 + 16 + t * 4);
+              }
+            }
+            float d[2], m[2];
+            scale_of(0, b, d[0], m[0]);
+            scale_of(1, b, d[1], m[1]);
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n) {
+              const uint4 x = *reinterpret_cast<const uint4*>(xf + ((blk * C::NT + n) * 32 + lane) * 16);
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (RT == ROW_Q4_K) {
+                if (i & 1) {
+                  mma_high(c, w0[0], w0[1], x.x, x.y);
+                  mma_high(c, w1[0], w1[1], x.z, x.w);
+                } else {
+                  mma_low(c, w0[0], w0[1], x.x, x.y);
+                  mma_low(c, w1[0], w1[1], x.z, x.w);
+                }
+              } else {
+                mma_low(c, w0[0], w0[1], x.x, x.y);
+                mma_high(c, w0[0], w0[1], x.z, x.w);
+              }
+#pragma unroll
+              for (int v = 0; v < AV; ++v) {
+                const float2 in = info[blk * C::VECS + (n * 4 + t) * AV + v];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const float s = C::PARTS == 2 ? c[2 * r] + c[2 * r + 1] : c[2 * r + v];
+                  acc[n][v][r] = fmaf(d[r] * in.x, s, acc[n][v][r]);
+                  acc[n][v][r] = fmaf(m[r], in.y, acc[n][v][r]);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      copy_step();
+    }
+    // ---- join the partial sums of the tile, in order ------------------------------------
+    float* mine = red + ((k & 1) * MV_WARPS + warp) * 16 * C::VECS;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int v = 0; v < AV; ++v)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float s = acc[n][v][r];
+          acc[n][v][r] = 0.f;
+          if constexpr (!C::MULTI) {
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if (t == 0) mine[g + 8 * r] = s;
+          } else {
+            mine[((n * 4 + t) * AV + v) * 16 + g + 8 * r] = s;
+          }
+        }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.ks * 32) : "memory");
+    for (int i = part * 32 + lane; i < 16 * nv; i += p.ks * 32) {
+      const int64_t row = (int64_t)tile * 16 + i % 16;
+      if (row >= p.a.rows) continue;
+      const float* from = red + ((k & 1) * MV_WARPS + group * p.ks) * 16 * C::VECS + i;
+      float s = 0.f;
+      for (int w = 0; w < p.ks; ++w) s += from[w * 16 * C::VECS];
+      if (p.a.bias) s += p.a.bias[row];
+      const int64_t at = (t0 + i / 16) * p.a.ys + row;
+      const bool add = (p.a.flags & MOE_ACCUMULATE) != 0;
+      if (p.a.y_type == MOE_F32) {
+        float* y = static_cast<float*>(p.a.y) + at;
+        *y = add ? *y + s : s;
+      } else if (p.a.y_type == MOE_F16) {
+        __half* y = static_cast<__half*>(p.a.y) + at;
+        *y = __float2half_rn(add ? __half2float(*y) + s : s);
+      } else {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.a.y) + at;
+        *y = __float2bfloat16_rn(add ? __bfloat162float(*y) + s : s);
+      }
+    }
+  }
+}
+
+constexpr int MV_CTAS = 304;            // two on each of 152 SMs
+constexpr int MV_SMEM = 227 * 1024;     // shared memory of a CTA at most
+
+// Shared memory: the rings, the x pieces and block sums, two sets of partial sums, a zero.
+template <int RT, class C>
+int smem_bytes(const MvArgs& p) {
+  const int stage = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
+  return MV_WARPS * MV_DEPTH * stage + p.nq * 128 * C::XBYTES + p.nq * 4 * C::VECS * 8 +
+         2 * MV_WARPS * 16 * C::VECS * 4 + 16;
+}
+
+template <int RT, class C>
+cudaError_t launch(MvArgs& p, cudaStream_t st) {
+  const int smem = smem_bytes<RT, C>(p);
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(matvec_kernel<RT, C>), smem);
+  if (e != cudaSuccess) return e;
+  const int ctas = smem <= 113 * 1024 ? MV_CTAS : MV_CTAS / 2;
+  // Warps that share a tile: the count whose slowest warp has the fewest runs to walk, and the
+  // larger one when two tie (fewer rows wait for a warp).
+  const int units = (p.nq + p.unit - 1) / p.unit;
+  int64_t best = -1;
+  for (int ks = MV_WARPS; ks >= 1; ks /= 2) {
+    const int per = MV_WARPS / ks;
+    const int64_t rounds = (p.tiles + (int64_t)ctas * per - 1) / ((int64_t)ctas * per);
+    const int64_t cost = rounds * ((units + ks - 1) / ks * p.unit * 4 + (ks > 1 ? 1 : 0));
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.ks = ks;
+    }
+  }
+  const int per = MV_WARPS / p.ks;
+  const int want = (p.tiles + per - 1) / per;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(want < ctas ? want : ctas), (unsigned)((p.a.T + C::VECS - 1) / C::VECS));
+  cfg.blockDim = dim3(MV_WARPS * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = p.pdl ? attr : nullptr;
+  cfg.numAttrs = p.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, matvec_kernel<RT, C>, p);
+}
+
+// The column form of a call. A pass of several vectors reads the weights once for all of
+// them but keeps 16 bytes of x pieces a value (32 for eight f32 vectors); rows too long for
+// that take the vectors one at a time.
+template <int RT>
+cudaError_t launch_cols(MvArgs& p, cudaStream_t st) {
+  const bool wide = p.a.x_type == MOE_F32;
+  if (p.a.T > 1 && !wide && smem_bytes<RT, Cols<true, 1, 1>>(p) <= MV_SMEM)
+    return launch<RT, Cols<true, 1, 1>>(p, st);
+  if (p.a.T > 4 && wide && smem_bytes<RT, Cols<true, 2, 2>>(p) <= MV_SMEM)
+    return launch<RT, Cols<true, 2, 2>>(p, st);
+  if (p.a.T > 1 && wide && smem_bytes<RT, Cols<true, 1, 2>>(p) <= MV_SMEM)
+    return launch<RT, Cols<true, 1, 2>>(p, st);
+  return launch<RT, Cols<false, 1, 2>>(p, st);
 }
 
 }  // namespace
 
 cudaError_t matvec_launch(const MatvecArgs& a, cudaStream_t st) {
-  if (a.x_type == MOE_F32) return launch_y<float>(a, st);
-  if (a.x_type == MOE_F16) return launch_y<__half>(a, st);
-  return launch_y<__nv_bfloat16>(a, st);
+  MvArgs p{};
+  p.a = a;
+  p.nb = a.cols / 32;
+  p.nq = (p.nb + 3) / 4;
+  p.unit = a.qtype == MOE_Q4_K ? 2 : 1;
+  p.tiles = (int)(((int64_t)a.rows + 15) / 16);
+  p.pdl = (a.flags & MOE_NO_PDL) == 0;
+  p.row_bytes = a.qtype == MOE_Q4_0 ? p.nb * 18 : a.qtype == MOE_Q4_1 ? p.nb * 20 : a.qtype == MOE_Q4_K ? p.nb * 18 : p.nb * 16;
+  p.total = p.row_bytes * a.rows;
+  if (a.qtype == MOE_Q4_PLANES) {
+    p.srow = a.cols / a.group * 2;
+    p.stotal = p.srow * a.rows;
+  }
+  switch (a.qtype) {
+    case MOE_Q4_0: return launch_cols<ROW_Q4_0>(p, st);
+    case MOE_Q4_1: return launch_cols<ROW_Q4_1>(p, st);
+    case MOE_Q4_K: return launch_cols<ROW_Q4_K>(p, st);
+    default: return launch_cols<ROW_PLANES>(p, st);
+  }
 }
 
 }  // namespace moe

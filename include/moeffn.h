@@ -283,7 +283,7 @@ int moe_ffn_forward_noalloc(const float* x, const float* router_w, const float* 
  *     values in the blocks' order (byte i: value i low, value 16 + i high); `scales` is
  *     [rows][cols / group] f16 and `mins` the same or NULL, group 32, 64 or 128, dividing
  *     cols; value = scale q + min, without mins scale (q - 8).
- * Limits: 1 <= rows; 32 <= cols <= 16384; n_vec >= 0 (0: nothing is launched). */
+ * Limits: 1 <= rows; 32 <= cols <= 16384; 0 <= n_vec <= 65535 (0: nothing is launched). */
 typedef struct moe_matvec_cfg {
   int32_t rows;
   int32_t cols;
