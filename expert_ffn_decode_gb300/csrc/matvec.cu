@@ -56,8 +56,7 @@ struct MvArgs {
   int64_t row_bytes, total;    // of the weights (planes: of the nibble plane)
   int64_t srow, stotal;        // planes: of the scales and of the offsets
   int nb;                      // blocks of a row
-  int nq;                      // runs of 128 values of a row (the last may be partial)
-  int unit;                    // runs that one warp takes whole: 2 for Q4_K (a super-block)
+  int nu;                      // runs of 256 values, 8 blocks, of a row (the last may be partial)
   int ks;                      // warps that share a tile of 16 rows
   int tiles;
   int pdl;
@@ -128,6 +127,10 @@ __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t
         quad = b / 4;
         t = (b >> 1 & 1) * 2 + r / 16;
         nib = b & 1;
+      } else if (RT == ROW_Q4_0) {  // every second block: 36 bytes apart, the quad's lanes meet four banks
+        quad = b / 8 * 2 + b % 2;
+        t = b / 2 & 3;
+        nib = r / 16;
       } else {
         quad = b / 4;
         t = b & 3;
@@ -170,8 +173,7 @@ __device__ __forceinline__ void copy16(void* dst, const uint8_t* src, int bytes)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
-// A warp's steps: the tiles of its group in turn, and in each its range of runs two at a time
-// (256 values). Each step's rows are copied to the warp's own ring, three steps ahead, so a
+// A warp's steps: the tiles of its group in turn, and in each its range of runs. Each step's rows are copied to the warp's own ring, three steps ahead, so a
 // warp never waits for another one but to join the partial sums of a tile.
 template <int RT, class C>
 __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_constant__ MvArgs p) {
@@ -180,52 +182,51 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   uint8_t* ring = sm + warp * MV_DEPTH * STAGE;
   uint8_t* xf = sm + MV_WARPS * MV_DEPTH * STAGE;
-  float2* info = reinterpret_cast<float2*>(xf + (size_t)(p.nq * 128) * C::XBYTES);
-  float* red = reinterpret_cast<float*>(info + p.nq * 4 * C::VECS);  // [2][warps][16 * VECS]
+  float2* info = reinterpret_cast<float2*>(xf + (size_t)(p.nu * 256) * C::XBYTES);
+  float* red = reinterpret_cast<float*>(info + p.nu * 8 * C::VECS);  // [2][warps][16 * VECS]
   float4* zero = reinterpret_cast<float4*>(red + 2 * MV_WARPS * 16 * C::VECS);
   const int groups = MV_WARPS / p.ks, group = warp / p.ks, part = warp % p.ks;
   const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
-  const int units = (p.nq + p.unit - 1) / p.unit;
-  const int qa = units * part / p.ks * p.unit, qb = min(units * (part + 1) / p.ks * p.unit, p.nq);
-  const int per_tile = (qb - qa + 1) / 2;
+  const int ua = p.nu * part / p.ks, ub = p.nu * (part + 1) / p.ks, per_tile = ub - ua;
   const int my_tiles = first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
   const int steps = my_tiles * per_tile;
+  // bytes of a row's full run
+  constexpr int RUN = RT == ROW_Q4_0 ? 144 : RT == ROW_Q4_1 ? 160 : RT == ROW_Q4_K ? 144 : 128;
+  constexpr int BLOCK = RUN / 8;
 
   if (p.pdl) pdl_launch_dependents();
   // ---- weights: the copies of one step -----------------------------------------------
-  int c_tile = first, c_q = qa, c_step = 0;  // the next step to copy
-  const int crow = lane >> 1;                // two lanes a row, 32 bytes a turn
+  // The 16 rows' windows in 16-byte pieces, consecutive pieces on consecutive lanes: an
+  // instruction then touches few lines. A tile's rows start at a multiple of 16 bytes, so a
+  // row's misalignment is that of the first tile's. The last row may end inside a piece.
+  constexpr int PIECES = RUN % 16 == 0 && (RT == ROW_Q4_K || RT == ROW_PLANES) ? RUN / 16 : RUN / 16 + 1;
+  int c_tile = first, c_u = ua, c_step = 0;  // the next step to copy
   auto copy_step = [&]() {
     if (c_step < steps) {
       uint8_t* dst = ring + c_step % MV_DEPTH * STAGE;
-      const int64_t row = (int64_t)c_tile * 16 + crow;
-      if (row < p.a.rows) {
-        const int runs = min(2, qb - c_q), blocks = min(runs * 4, p.nb - c_q * 4);
-        const int64_t from = row * p.row_bytes +
-                             (RT == ROW_Q4_0 ? c_q * 72 : RT == ROW_Q4_1 ? c_q * 80 : RT == ROW_Q4_K ? c_q / 2 * 144 : c_q * 64);
-        const int bytes = RT == ROW_Q4_0 ? blocks * 18 : RT == ROW_Q4_1 ? blocks * 20 : RT == ROW_Q4_K ? 144 : blocks * 16;
-        const int64_t lo = from & ~(int64_t)15;
-        const int n = (int)(from + bytes - lo);  // bytes of the window up to the last one wanted
+      const int64_t base = (int64_t)c_tile * 16 * p.row_bytes;
+      const int rows = min(16, p.a.rows - c_tile * 16), bytes = min(8, p.nb - c_u * 8) * BLOCK;
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {
-          const int at = (2 * i + (lane & 1)) * 16;
-          // the last piece stops at the array's end
-          if (at < n) copy16(dst + crow * MV_PITCH + at, p.a.w + lo + at, (int)min((int64_t)16, p.total - lo - at));
+      for (int i = 0; i < (16 * PIECES + 31) / 32; ++i) {
+        const int at = i * 32 + lane, r = at / PIECES, c = at % PIECES * 16;
+        const int from = r * (int)p.row_bytes + c_u * RUN, lo = from & ~15;
+        if (r < rows && lo + c < from + bytes) {
+          const int64_t src = base + lo + c;
+          copy16(dst + r * MV_PITCH + c, p.a.w + src, (int)min((int64_t)16, p.total - src));
         }
-        if constexpr (RT == ROW_PLANES) {
-          const int64_t sf = (row * (p.a.cols / p.a.group) + c_q * 128 / p.a.group) * 2, sl = sf & ~(int64_t)15;
-          const int at = (lane & 1) * 16;
-          const int left = (int)min((int64_t)16, p.stotal - sl - at);
-          if (left > 0) {
-            copy16(dst + 16 * MV_PITCH + crow * MV_SPITCH + at, p.a.scales + sl + at, left);
-            if (p.a.mins) copy16(dst + 16 * (MV_PITCH + MV_SPITCH) + crow * MV_SPITCH + at, p.a.mins + sl + at, left);
-          }
+      }
+      if constexpr (RT == ROW_PLANES) {
+        const int r = lane >> 1, at = (lane & 1) * 16;
+        const int64_t sl = (((int64_t)c_tile * 16 + r) * p.srow + c_u * 256 / p.a.group * 2 & ~(int64_t)15) + at;
+        const int left = (int)min((int64_t)16, p.stotal - sl);
+        if (r < rows && left > 0) {
+          copy16(dst + 16 * MV_PITCH + r * MV_SPITCH + at, p.a.scales + sl, left);
+          if (p.a.mins) copy16(dst + 16 * (MV_PITCH + MV_SPITCH) + r * MV_SPITCH + at, p.a.mins + sl, left);
         }
       }
       ++c_step;
-      c_q += 2;
-      if (c_q >= qb) {
-        c_q = qa;
+      if (++c_u == ub) {
+        c_u = ua;
         c_tile += stride;
       }
     }
@@ -262,24 +263,32 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
 #pragma unroll
     for (int v = 0; v < AV; ++v) acc[n][v][0] = acc[n][v][1] = 0.f;
 
+  // where the two rows' windows start in a stage, and their scales'
+  const int row_at[2] = {g * MV_PITCH, (g + 8) * MV_PITCH};
+  uint4 x[2][4];  // single vector: the pieces of a run, kept from tile to tile if there is one run
   int step = 0;
   for (int k = 0, tile = first; k < my_tiles; ++k, tile += stride) {
-    for (int q0 = qa; q0 < qb; q0 += 2, ++step) {
+    for (int u0 = ua; u0 < ub; ++u0, ++step) {
+      if constexpr (!C::MULTI) {
+        if (step == 0 || per_tile > 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i / 4][i % 4] = *reinterpret_cast<const uint4*>(
+                xl[i / 2 % 2] + (xstep[i / 2 % 2] ? (u0 * 2 + i / 4) * 512 + (i & 1) * 128 : 0));
+        }
+      }
       asm volatile("cp.async.wait_group %0;" ::"n"(MV_DEPTH - 2) : "memory");
       __syncwarp();
       const uint8_t* st = ring + step % MV_DEPTH * STAGE;
-      // where the two rows' windows start in the stage, and their scales'
       const uint8_t* base[2];
       const uint8_t* sbase[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int64_t row = (int64_t)tile * 16 + g + 8 * r;
-        int mis = 0;
-        if (RT == ROW_Q4_0) mis = (int)((row * p.row_bytes + q0 * 72) & 15);
-        if (RT == ROW_Q4_1) mis = (int)((row * p.row_bytes + q0 * 80) & 15);
-        base[r] = st + (g + 8 * r) * MV_PITCH + mis;
+        base[r] = st + row_at[r];
+        if (RT == ROW_Q4_0 || RT == ROW_Q4_1) base[r] += (g + 8 * r) * (int)p.row_bytes + u0 * RUN & 15;
         sbase[r] = st + 16 * MV_PITCH + (g + 8 * r) * MV_SPITCH;
-        if (RT == ROW_PLANES) sbase[r] += (int)((row * (p.a.cols / p.a.group) + q0 * 128 / p.a.group) * 2 & 15);
+        if (RT == ROW_PLANES)
+          sbase[r] += (int)(((int64_t)tile * 16 + g + 8 * r) * p.srow + u0 * 256 / p.a.group * 2 & 15);
       }
       // word i of block b (of the step) of row r, and the block's scale and offset
       auto scale_of = [&](int r, int b, float& d, float& m) {
@@ -300,59 +309,57 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
       };
 #pragma unroll
       for (int qq = 0; qq < 2; ++qq) {
-        const int quad = q0 + qq;
-        if (quad >= qb) break;
         if constexpr (!C::MULTI) {
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(xl[i / 2] + (xstep[i / 2] ? quad * 512 + (i & 1) * 128 : 0));
-          const int b = qq * 4 + t;  // this lane's block of the step
+          const int b = RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t;  // this lane's block of the run
+          float dd[2], mm[2];
           uint32_t w[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             if constexpr (RT == ROW_Q4_0) {
               const uint8_t* s = base[r] + b * 18;
               const uint32_t* u = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(s) & ~(uintptr_t)3);
-              const uint32_t sh = reinterpret_cast<uintptr_t>(s) & 2 ? 32 : 16;
+              const bool odd = (reinterpret_cast<uintptr_t>(s) & 2) != 0;
               uint32_t v[5];
 #pragma unroll
               for (int i = 0; i < 5; ++i) v[i] = u[i];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[r][i] = __funnelshift_rc(v[i], v[i + 1], sh);
+              for (int i = 0; i < 4; ++i) w[r][i] = __funnelshift_rc(v[i], v[i + 1], odd ? 32 : 16);
+              dd[r] = half_bits(odd ? v[0] >> 16 : v[0] & 0xffffu);
+              mm[r] = -8.f * dd[r];
             } else if constexpr (RT == ROW_Q4_1) {
-              const uint32_t* u = reinterpret_cast<const uint32_t*>(base[r] + b * 20 + 4);
+              const uint32_t* u = reinterpret_cast<const uint32_t*>(base[r] + b * 20);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[r][i] = u[i];
+              for (int i = 0; i < 4; ++i) w[r][i] = u[i + 1];
+              dd[r] = half_bits(u[0] & 0xffffu);
+              mm[r] = half_bits(u[0] >> 16);
             } else {
               const uint4 u = *reinterpret_cast<const uint4*>(base[r] + (RT == ROW_Q4_K ? 16 : 0) + b * 16);
               w[r][0] = u.x;
               w[r][1] = u.y;
               w[r][2] = u.z;
               w[r][3] = u.w;
+              scale_of(r, b, dd[r], mm[r]);
             }
           }
           float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            mma_low(c, w[0][j], w[1][j], j & 1 ? x[j / 2].z : x[j / 2].x, j & 1 ? x[j / 2].w : x[j / 2].y);
-            mma_high(c, w[0][j], w[1][j], j & 1 ? x[2 + j / 2].z : x[2 + j / 2].x,
-                     j & 1 ? x[2 + j / 2].w : x[2 + j / 2].y);
+            const uint4 xa = x[qq][j / 2], xb = x[qq][2 + j / 2];
+            mma_low(c, w[0][j], w[1][j], j & 1 ? xa.z : xa.x, j & 1 ? xa.w : xa.y);
+            mma_high(c, w[0][j], w[1][j], j & 1 ? xb.z : xb.x, j & 1 ? xb.w : xb.y);
           }
-          if (quad * 4 + t < p.nb) {
-            const float2 in = info[quad * 4 + t];
+          if (u0 * 8 + b < p.nb) {
+            const float2 in = info[u0 * 8 + b];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float d, m;
-              scale_of(r, b, d, m);
-              acc[0][0][r] = fmaf(d * in.x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
-              acc[0][0][r] = fmaf(m, in.y, acc[0][0][r]);
+              acc[0][0][r] = fmaf(dd[r] * in.x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
+              acc[0][0][r] = fmaf(mm[r], in.y, acc[0][0][r]);
             }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int b = qq * 4 + i, blk = quad * 4 + i;
+            const int b = qq * 4 + i, blk = u0 * 8 + b;
             if (blk >= p.nb) break;
             uint32_t w0[2], w1[2];  // the words of the first and the second 16 values
 #pragma unroll
@@ -454,7 +461,7 @@ constexpr int MV_SMEM = 227 * 1024;     // shared memory of a CTA at most
 template <int RT, class C>
 int smem_bytes(const MvArgs& p) {
   const int stage = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
-  return MV_WARPS * MV_DEPTH * stage + p.nq * 128 * C::XBYTES + p.nq * 4 * C::VECS * 8 +
+  return MV_WARPS * MV_DEPTH * stage + p.nu * 256 * C::XBYTES + p.nu * 8 * C::VECS * 8 +
          2 * MV_WARPS * 16 * C::VECS * 4 + 16;
 }
 
@@ -466,12 +473,11 @@ cudaError_t launch(MvArgs& p, cudaStream_t st) {
   const int ctas = smem <= 113 * 1024 ? MV_CTAS : MV_CTAS / 2;
   // Warps that share a tile: the count whose slowest warp has the fewest runs to walk, and the
   // larger one when two tie (fewer rows wait for a warp).
-  const int units = (p.nq + p.unit - 1) / p.unit;
   int64_t best = -1;
   for (int ks = MV_WARPS; ks >= 1; ks /= 2) {
     const int per = MV_WARPS / ks;
     const int64_t rounds = (p.tiles + (int64_t)ctas * per - 1) / ((int64_t)ctas * per);
-    const int64_t cost = rounds * ((units + ks - 1) / ks * p.unit * 4 + (ks > 1 ? 1 : 0));
+    const int64_t cost = rounds * ((p.nu + ks - 1) / ks * 8 + (ks > 1 ? 1 : 0));
     if (best < 0 || cost < best) {
       best = cost;
       p.ks = ks;
@@ -513,8 +519,7 @@ cudaError_t matvec_launch(const MatvecArgs& a, cudaStream_t st) {
   MvArgs p{};
   p.a = a;
   p.nb = a.cols / 32;
-  p.nq = (p.nb + 3) / 4;
-  p.unit = a.qtype == MOE_Q4_K ? 2 : 1;
+  p.nu = (p.nb + 7) / 8;
   p.tiles = (int)(((int64_t)a.rows + 15) / 16);
   p.pdl = (a.flags & MOE_NO_PDL) == 0;
   p.row_bytes = a.qtype == MOE_Q4_0 ? p.nb * 18 : a.qtype == MOE_Q4_1 ? p.nb * 20 : a.qtype == MOE_Q4_K ? p.nb * 18 : p.nb * 16;
