@@ -92,63 +92,68 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // x in f16 pieces, and for each block and vector {2^10 / scale, sum of x}. A thread takes four
 // values of a vector; the eight threads of a block are neighbours. Values past the row's end
 // are not written: they belong to blocks whose sums are dropped.
+template <int RT, class C>
+__device__ __forceinline__ void put_x(float4 v, int vec, int at, uint8_t* xf, float2* info) {
+  float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+  float sum = (v.x + v.y) + (v.z + v.w);
+  const unsigned group = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
+    sum += __shfl_xor_sync(group, sum, o);
+  }
+  // largest magnitude 2^e (1 .. 2): scale 2^(13 - e); it and 2^10 / it stay normal
+  const int e = min(max((int)(__float_as_uint(mx) >> 23), 27), 253);
+  const float sc = __uint_as_float((uint32_t)(267 - e) << 23);
+  const float back = __uint_as_float((uint32_t)(e - 13) << 23);  // 1 / sc
+  const int b = at / 32, r = at % 32;
+  const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
+  float hi[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    hi[j] = __half2float(__float2half_rn(f[j]));
+    lo[j] = f[j] - hi[j];
+  }
+  const uint2 parts[2] = {make_uint2(pack_h2(hi[0], hi[2]), pack_h2(hi[1], hi[3])),
+                          make_uint2(pack_h2(lo[0], lo[2]), pack_h2(lo[1], lo[3]))};
+  if constexpr (!C::MULTI) {
+    int quad = b / 4, t = b & 3, nib = r / 16;
+    if (RT == ROW_Q4_K) {  // lane t: 16 bytes, half t % 2 of a run of 64; nibble: which sub-block of it
+      t = (b >> 1 & 1) * 2 + r / 16;
+      nib = b & 1;
+    } else if (RT == ROW_Q4_0) {  // every second block: 36 bytes apart, the quad's lanes meet four banks
+      quad = b / 8 * 2 + b % 2;
+      t = b / 2 & 3;
+    }
+    const int j = r % 16 / 4;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<uint2*>(xf + quad * 512 + (nib * 2 + j / 2) * 128 + (2 * t + q) * 16 + j % 2 * 8) = parts[q];
+  } else {
+#pragma unroll
+    for (int q = 0; q < C::PARTS; ++q) {
+      const int col = vec * C::PARTS + q, lane = col % 8 * 4 + r % 16 / 4;
+      *reinterpret_cast<uint2*>(xf + ((b * C::NT + col / 8) * 32 + lane) * 16 + r / 16 * 8) = parts[q];
+    }
+  }
+  if ((threadIdx.x & 7) == 0) info[b * C::VECS + vec] = make_float2(back * 1024.f, sum);
+}
 template <int RT, class C, typename TX>
 __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t* xf, float2* info) {
   const TX* x = static_cast<const TX*>(p.a.x) + t0 * p.a.xs;
-  const int per = p.a.cols / 4;
-  for (int i = threadIdx.x; i < per * nv; i += MV_WARPS * 32) {  // a block's 8 threads stay together
-    const int vec = i / per, at = i % per * 4;
-    const float4 v = load4(x + vec * p.a.xs + at);
-    float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-    float sum = (v.x + v.y) + (v.z + v.w);
-    const unsigned group = 0xffu << (threadIdx.x & 24);
+  constexpr int AHEAD = 4, NTH = MV_WARPS * 32;  // loads in flight of a thread
+  const int per = p.a.cols / 4, total = per * nv;  // a multiple of 8: a block's 8 threads stay together
+  for (int i0 = threadIdx.x; i0 < total; i0 += NTH * AHEAD) {
+    float4 ld[AHEAD];
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
-      sum += __shfl_xor_sync(group, sum, o);
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = min(i0 + n * NTH, total - 1);
+      ld[n] = load4(x + i / per * p.a.xs + i % per * 4);
     }
-    // largest magnitude 2^e (1 .. 2): scale 2^(13 - e); it and 2^10 / it stay normal
-    const int e = min(max((int)(__float_as_uint(mx) >> 23), 27), 253);
-    const float sc = __uint_as_float((uint32_t)(267 - e) << 23);
-    const float back = __uint_as_float((uint32_t)(e - 13) << 23);  // 1 / sc
-    const int b = at / 32, r = at % 32;
-    const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
-    float hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      hi[j] = __half2float(__float2half_rn(f[j]));
-      lo[j] = f[j] - hi[j];
-    }
-    const uint2 parts[2] = {make_uint2(pack_h2(hi[0], hi[2]), pack_h2(hi[1], hi[3])),
-                            make_uint2(pack_h2(lo[0], lo[2]), pack_h2(lo[1], lo[3]))};
-    if constexpr (!C::MULTI) {
-      int quad, t, nib;
-      if (RT == ROW_Q4_K) {  // lane t: 16 bytes, half t % 2 of a run; nibble: which sub-block of the run
-        quad = b / 4;
-        t = (b >> 1 & 1) * 2 + r / 16;
-        nib = b & 1;
-      } else if (RT == ROW_Q4_0) {  // every second block: 36 bytes apart, the quad's lanes meet four banks
-        quad = b / 8 * 2 + b % 2;
-        t = b / 2 & 3;
-        nib = r / 16;
-      } else {
-        quad = b / 4;
-        t = b & 3;
-        nib = r / 16;
-      }
-      const int j = r % 16 / 4;
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *reinterpret_cast<uint2*>(xf + quad * 512 + (nib * 2 + j / 2) * 128 + (2 * t + q) * 16 + j % 2 * 8) = parts[q];
-      if ((threadIdx.x & 7) == 0) info[b] = make_float2(back * 1024.f, sum);
-    } else {
-#pragma unroll
-      for (int q = 0; q < C::PARTS; ++q) {
-        const int n = vec * C::PARTS + q;
-        const int lane = n % 8 * 4 + r % 16 / 4;
-        *reinterpret_cast<uint2*>(xf + ((b * C::NT + n / 8) * 32 + lane) * 16 + r / 16 * 8) = parts[q];
-      }
-      if ((threadIdx.x & 7) == 0) info[b * C::VECS + vec] = make_float2(back * 1024.f, sum);
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = i0 + n * NTH;
+      if (i < total) put_x<RT, C>(ld[n], i / per, i % per * 4, xf, info);
     }
   }
 }
@@ -197,34 +202,46 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
   if (p.pdl) pdl_launch_dependents();
   // ---- weights: the copies of one step -----------------------------------------------
   // The 16 rows' windows in 16-byte pieces, consecutive pieces on consecutive lanes: an
-  // instruction then touches few lines. A tile's rows start at a multiple of 16 bytes, so a
-  // row's misalignment is that of the first tile's. The last row may end inside a piece.
-  constexpr int PIECES = RUN % 16 == 0 && (RT == ROW_Q4_K || RT == ROW_PLANES) ? RUN / 16 : RUN / 16 + 1;
-  int c_tile = first, c_u = ua, c_step = 0;  // the next step to copy
-  auto copy_step = [&]() {
-    if (c_step < steps) {
-      uint8_t* dst = ring + c_step % MV_DEPTH * STAGE;
-      const int64_t base = (int64_t)c_tile * 16 * p.row_bytes;
-      const int rows = min(16, p.a.rows - c_tile * 16), bytes = min(8, p.nb - c_u * 8) * BLOCK;
+  // instruction then touches few lines. Tiles and full runs start at multiples of 16 bytes,
+  // so where a lane's pieces are within them never changes.
+  constexpr int PIECES = RT == ROW_Q4_K || RT == ROW_PLANES ? RUN / 16 : RUN / 16 + 1;
+  constexpr int TURNS = (16 * PIECES + 31) / 32;
+  int from[TURNS], to[TURNS];  // a piece's place in the tile's bytes (run 0) and in the stage
 #pragma unroll
-      for (int i = 0; i < (16 * PIECES + 31) / 32; ++i) {
-        const int at = i * 32 + lane, r = at / PIECES, c = at % PIECES * 16;
-        const int from = r * (int)p.row_bytes + c_u * RUN, lo = from & ~15;
-        if (r < rows && lo + c < from + bytes) {
-          const int64_t src = base + lo + c;
-          copy16(dst + r * MV_PITCH + c, p.a.w + src, (int)min((int64_t)16, p.total - src));
+  for (int i = 0; i < TURNS; ++i) {
+    const int at = i * 32 + lane, r = at / PIECES, c = at % PIECES * 16, b = r * (int)p.row_bytes;
+    to[i] = r * MV_PITCH + c;
+    from[i] = r < 16 && (b & ~15) + c < b + RUN ? (b & ~15) + c : -1;
+  }
+  int c_tile = first, c_u = ua, c_left = steps, c_at = 0;  // the next step to copy, and its stage
+  auto copy_step = [&]() {
+    if (c_left > 0) {
+      uint8_t* dst = ring + c_at;
+      const int64_t base = (int64_t)c_tile * 16 * p.row_bytes + c_u * RUN;
+      if (c_tile + 1 < p.tiles && c_u * 8 + 8 <= p.nb) {
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i)
+          if (from[i] >= 0) copy16(dst + to[i], p.a.w + base + from[i], 16);
+      } else {  // fewer rows, a partial run, and a last row that may end inside a piece
+        const int rows = min(16, p.a.rows - c_tile * 16), bytes = min(8, p.nb - c_u * 8) * BLOCK;
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+          const int r = (i * 32 + lane) / PIECES;
+          if (from[i] >= 0 && r < rows && from[i] < r * (int)p.row_bytes + bytes)
+            copy16(dst + to[i], p.a.w + base + from[i], (int)min((int64_t)16, p.total - base - from[i]));
         }
       }
       if constexpr (RT == ROW_PLANES) {
         const int r = lane >> 1, at = (lane & 1) * 16;
-        const int64_t sl = (((int64_t)c_tile * 16 + r) * p.srow + c_u * 256 / p.a.group * 2 & ~(int64_t)15) + at;
+        const int64_t sl = ((((int64_t)c_tile * 16 + r) * p.srow + c_u * 256 / p.a.group * 2) & ~(int64_t)15) + at;
         const int left = (int)min((int64_t)16, p.stotal - sl);
-        if (r < rows && left > 0) {
+        if (c_tile * 16 + r < p.a.rows && left > 0) {
           copy16(dst + 16 * MV_PITCH + r * MV_SPITCH + at, p.a.scales + sl, left);
           if (p.a.mins) copy16(dst + 16 * (MV_PITCH + MV_SPITCH) + r * MV_SPITCH + at, p.a.mins + sl, left);
         }
       }
-      ++c_step;
+      --c_left;
+      c_at = c_at == (MV_DEPTH - 1) * STAGE ? 0 : c_at + STAGE;
       if (++c_u == ub) {
         c_u = ua;
         c_tile += stride;
@@ -264,13 +281,19 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
     for (int v = 0; v < AV; ++v) acc[n][v][0] = acc[n][v][1] = 0.f;
 
   // where the two rows' windows start in a stage, and their scales'
-  const int row_at[2] = {g * MV_PITCH, (g + 8) * MV_PITCH};
+  int row_at[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    row_at[r] = (g + 8 * r) * MV_PITCH + (((g + 8 * r) * (int)p.row_bytes) & 15);
   uint4 x[2][4];  // single vector: the pieces of a run, kept from tile to tile if there is one run
-  int step = 0;
+  float2 xin[2];
+  int stage = 0;
   for (int k = 0, tile = first; k < my_tiles; ++k, tile += stride) {
-    for (int u0 = ua; u0 < ub; ++u0, ++step) {
+    for (int u0 = ua; u0 < ub; ++u0) {
       if constexpr (!C::MULTI) {
-        if (step == 0 || per_tile > 1) {
+        if (k == 0 || per_tile > 1) {
+#pragma unroll
+          for (int qq = 0; qq < 2; ++qq) xin[qq] = info[u0 * 8 + (RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t)];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             x[i / 4][i % 4] = *reinterpret_cast<const uint4*>(
@@ -279,16 +302,16 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(MV_DEPTH - 2) : "memory");
       __syncwarp();
-      const uint8_t* st = ring + step % MV_DEPTH * STAGE;
+      const uint8_t* st = ring + stage;
+      stage = stage == (MV_DEPTH - 1) * STAGE ? 0 : stage + STAGE;
       const uint8_t* base[2];
       const uint8_t* sbase[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         base[r] = st + row_at[r];
-        if (RT == ROW_Q4_0 || RT == ROW_Q4_1) base[r] += (g + 8 * r) * (int)p.row_bytes + u0 * RUN & 15;
         sbase[r] = st + 16 * MV_PITCH + (g + 8 * r) * MV_SPITCH;
         if (RT == ROW_PLANES)
-          sbase[r] += (int)(((int64_t)tile * 16 + g + 8 * r) * p.srow + u0 * 256 / p.a.group * 2 & 15);
+          sbase[r] += ((g + 8 * r) * (int)p.srow + u0 * 256 / p.a.group * 2) & 15;
       }
       // word i of block b (of the step) of row r, and the block's scale and offset
       auto scale_of = [&](int r, int b, float& d, float& m) {
@@ -349,11 +372,10 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
             mma_high(c, w[0][j], w[1][j], j & 1 ? xb.z : xb.x, j & 1 ? xb.w : xb.y);
           }
           if (u0 * 8 + b < p.nb) {
-            const float2 in = info[u0 * 8 + b];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              acc[0][0][r] = fmaf(dd[r] * in.x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
-              acc[0][0][r] = fmaf(mm[r], in.y, acc[0][0][r]);
+              acc[0][0][r] = fmaf(dd[r] * xin[qq].x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
+              acc[0][0][r] = fmaf(mm[r], xin[qq].y, acc[0][0][r]);
             }
           }
         } else {
