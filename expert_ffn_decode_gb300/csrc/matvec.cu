@@ -68,6 +68,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // The nibbles of word w (rows g) and u (rows g + 8) against x pieces: low nibbles are values
 // 4 j .. 4 j + 3 of a half block in the order 0, 2 | 1, 3, high ones of the other half.
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
@@ -77,11 +83,15 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t low_h2(uint32_t w) { return mul_h2(w & 0x000f000fu, 0x74007400u); }   // 2^14
 __device__ __forceinline__ uint32_t high_h2(uint32_t w) { return mul_h2(w & 0x00f000f0u, 0x64006400u); }  // 2^10
+template <bool first>
 __device__ __forceinline__ void mma_low(float (&c)[4], uint32_t w, uint32_t u, uint32_t b0, uint32_t b1) {
-  mma16816(c, low_h2(w), low_h2(u), low_h2(w >> 8), low_h2(u >> 8), b0, b1);
+  if (first) mma16816_zero(c, low_h2(w), low_h2(u), low_h2(w >> 8), low_h2(u >> 8), b0, b1);
+  else mma16816(c, low_h2(w), low_h2(u), low_h2(w >> 8), low_h2(u >> 8), b0, b1);
 }
+template <bool first>
 __device__ __forceinline__ void mma_high(float (&c)[4], uint32_t w, uint32_t u, uint32_t b0, uint32_t b1) {
-  mma16816(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
+  if (first) mma16816_zero(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
+  else mma16816(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
 }
 __device__ __forceinline__ float half_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -174,8 +184,8 @@ __device__ __forceinline__ void q4k_scale(uint4 h, int j, float& d, float& m) {
   m = -half_bits(h.x >> 16) * (float)mn;
 }
 
-__device__ __forceinline__ void copy16(void* dst, const uint8_t* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // A warp's steps: the tiles of its group in turn, and in each its range of runs. Each step's rows are copied to the warp's own ring, three steps ahead, so a
@@ -213,22 +223,24 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
     to[i] = r * MV_PITCH + c;
     from[i] = r < 16 && (b & ~15) + c < b + RUN ? (b & ~15) + c : -1;
   }
-  int c_tile = first, c_u = ua, c_left = steps, c_at = 0;  // the next step to copy, and its stage
+  int c_tile = first, c_u = ua, c_left = steps;  // the next step to copy
+  uint32_t c_at = smem_addr(ring);               // its stage
+  const uint8_t* c_src = p.a.w + (int64_t)first * 16 * p.row_bytes + ua * RUN;
+  const int64_t next_tile = (int64_t)stride * 16 * p.row_bytes - (int64_t)(per_tile - 1) * RUN;
+  const uint32_t ring_end = c_at + (MV_DEPTH - 1) * STAGE;
   auto copy_step = [&]() {
     if (c_left > 0) {
-      uint8_t* dst = ring + c_at;
-      const int64_t base = (int64_t)c_tile * 16 * p.row_bytes + c_u * RUN;
       if (c_tile + 1 < p.tiles && c_u * 8 + 8 <= p.nb) {
 #pragma unroll
         for (int i = 0; i < TURNS; ++i)
-          if (from[i] >= 0) copy16(dst + to[i], p.a.w + base + from[i], 16);
+          if (from[i] >= 0) copy16(c_at + to[i], c_src + from[i], 16);
       } else {  // fewer rows, a partial run, and a last row that may end inside a piece
         const int rows = min(16, p.a.rows - c_tile * 16), bytes = min(8, p.nb - c_u * 8) * BLOCK;
 #pragma unroll
         for (int i = 0; i < TURNS; ++i) {
           const int r = (i * 32 + lane) / PIECES;
           if (from[i] >= 0 && r < rows && from[i] < r * (int)p.row_bytes + bytes)
-            copy16(dst + to[i], p.a.w + base + from[i], (int)min((int64_t)16, p.total - base - from[i]));
+            copy16(c_at + to[i], c_src + from[i], (int)min((int64_t)16, p.a.w + p.total - (c_src + from[i])));
         }
       }
       if constexpr (RT == ROW_PLANES) {
@@ -236,15 +248,18 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
         const int64_t sl = ((((int64_t)c_tile * 16 + r) * p.srow + c_u * 256 / p.a.group * 2) & ~(int64_t)15) + at;
         const int left = (int)min((int64_t)16, p.stotal - sl);
         if (c_tile * 16 + r < p.a.rows && left > 0) {
-          copy16(dst + 16 * MV_PITCH + r * MV_SPITCH + at, p.a.scales + sl, left);
-          if (p.a.mins) copy16(dst + 16 * (MV_PITCH + MV_SPITCH) + r * MV_SPITCH + at, p.a.mins + sl, left);
+          copy16(c_at + 16 * MV_PITCH + r * MV_SPITCH + at, p.a.scales + sl, left);
+          if (p.a.mins) copy16(c_at + 16 * (MV_PITCH + MV_SPITCH) + r * MV_SPITCH + at, p.a.mins + sl, left);
         }
       }
       --c_left;
-      c_at = c_at == (MV_DEPTH - 1) * STAGE ? 0 : c_at + STAGE;
+      c_at = c_at == ring_end ? ring_end - (MV_DEPTH - 1) * STAGE : c_at + STAGE;
       if (++c_u == ub) {
         c_u = ua;
         c_tile += stride;
+        c_src += next_tile;
+      } else {
+        c_src += RUN;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -285,6 +300,16 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
 #pragma unroll
   for (int r = 0; r < 2; ++r)
     row_at[r] = (g + 8 * r) * MV_PITCH + (((g + 8 * r) * (int)p.row_bytes) & 15);
+  // Q4_0, single vector: a block starts on 2 bytes, so its words are funnelled from aligned ones;
+  // where they are and by how much is the lane's own, whatever the tile
+  int word_at[2][2];
+  uint32_t word_shift[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = row_at[i / 2] + (2 * t + i % 2) * 18;
+    word_at[i / 2][i % 2] = at & ~3;
+    word_shift[i / 2][i % 2] = at & 2 ? 32 : 16;
+  }
   uint4 x[2][4];  // single vector: the pieces of a run, kept from tile to tile if there is one run
   float2 xin[2];
   int stage = 0;
@@ -293,7 +318,10 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
       if constexpr (!C::MULTI) {
         if (k == 0 || per_tile > 1) {
 #pragma unroll
-          for (int qq = 0; qq < 2; ++qq) xin[qq] = info[u0 * 8 + (RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t)];
+          for (int qq = 0; qq < 2; ++qq) {
+            xin[qq] = info[u0 * 8 + (RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t)];
+            if (RT == ROW_Q4_0) xin[qq].y *= -8.f;
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             x[i / 4][i % 4] = *reinterpret_cast<const uint4*>(
@@ -339,16 +367,13 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             if constexpr (RT == ROW_Q4_0) {
-              const uint8_t* s = base[r] + b * 18;
-              const uint32_t* u = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(s) & ~(uintptr_t)3);
-              const bool odd = (reinterpret_cast<uintptr_t>(s) & 2) != 0;
+              const uint32_t* u = reinterpret_cast<const uint32_t*>(st + word_at[r][qq]);
               uint32_t v[5];
 #pragma unroll
               for (int i = 0; i < 5; ++i) v[i] = u[i];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[r][i] = __funnelshift_rc(v[i], v[i + 1], odd ? 32 : 16);
-              dd[r] = half_bits(odd ? v[0] >> 16 : v[0] & 0xffffu);
-              mm[r] = -8.f * dd[r];
+              for (int i = 0; i < 4; ++i) w[r][i] = __funnelshift_rc(v[i], v[i + 1], word_shift[r][qq]);
+              dd[r] = half_bits((v[0] >> (word_shift[r][qq] & 16 ^ 16)) & 0xffffu);
             } else if constexpr (RT == ROW_Q4_1) {
               const uint32_t* u = reinterpret_cast<const uint32_t*>(base[r] + b * 20);
 #pragma unroll
@@ -364,18 +389,24 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
               scale_of(r, b, dd[r], mm[r]);
             }
           }
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 xa = x[qq][j / 2], xb = x[qq][2 + j / 2];
-            mma_low(c, w[0][j], w[1][j], j & 1 ? xa.z : xa.x, j & 1 ? xa.w : xa.y);
-            mma_high(c, w[0][j], w[1][j], j & 1 ? xb.z : xb.x, j & 1 ? xb.w : xb.y);
-          }
+          float c[4];
+          mma_low<true>(c, w[0][0], w[1][0], x[qq][0].x, x[qq][0].y);
+          mma_high<false>(c, w[0][0], w[1][0], x[qq][2].x, x[qq][2].y);
+          mma_low<false>(c, w[0][1], w[1][1], x[qq][0].z, x[qq][0].w);
+          mma_high<false>(c, w[0][1], w[1][1], x[qq][2].z, x[qq][2].w);
+          mma_low<false>(c, w[0][2], w[1][2], x[qq][1].x, x[qq][1].y);
+          mma_high<false>(c, w[0][2], w[1][2], x[qq][3].x, x[qq][3].y);
+          mma_low<false>(c, w[0][3], w[1][3], x[qq][1].z, x[qq][1].w);
+          mma_high<false>(c, w[0][3], w[1][3], x[qq][3].z, x[qq][3].w);
           if (u0 * 8 + b < p.nb) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              acc[0][0][r] = fmaf(dd[r] * xin[qq].x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
-              acc[0][0][r] = fmaf(mm[r], xin[qq].y, acc[0][0][r]);
+              if (RT == ROW_Q4_0) {  // d (sum q x - 8 sum x)
+                acc[0][0][r] = fmaf(dd[r], fmaf(xin[qq].x, c[2 * r] + c[2 * r + 1], xin[qq].y), acc[0][0][r]);
+              } else {
+                acc[0][0][r] = fmaf(dd[r] * xin[qq].x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
+                acc[0][0][r] = fmaf(mm[r], xin[qq].y, acc[0][0][r]);
+              }
             }
           }
         } else {
@@ -404,18 +435,18 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
               const uint4 x = *reinterpret_cast<const uint4*>(xf + ((blk * C::NT + n) * 32 + lane) * 16);
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              float c[4];
               if constexpr (RT == ROW_Q4_K) {
                 if (i & 1) {
-                  mma_high(c, w0[0], w0[1], x.x, x.y);
-                  mma_high(c, w1[0], w1[1], x.z, x.w);
+                  mma_high<true>(c, w0[0], w0[1], x.x, x.y);
+                  mma_high<false>(c, w1[0], w1[1], x.z, x.w);
                 } else {
-                  mma_low(c, w0[0], w0[1], x.x, x.y);
-                  mma_low(c, w1[0], w1[1], x.z, x.w);
+                  mma_low<true>(c, w0[0], w0[1], x.x, x.y);
+                  mma_low<false>(c, w1[0], w1[1], x.z, x.w);
                 }
               } else {
-                mma_low(c, w0[0], w0[1], x.x, x.y);
-                mma_high(c, w0[0], w0[1], x.z, x.w);
+                mma_low<true>(c, w0[0], w0[1], x.x, x.y);
+                mma_high<false>(c, w0[0], w0[1], x.z, x.w);
               }
 #pragma unroll
               for (int v = 0; v < AV; ++v) {
