@@ -13,13 +13,17 @@
 // is one operand for two products, S^T comes from tensor memory without a pass through
 // shared memory, and a thread owns half a row of S^T in f32 registers.
 //
-// Rounding: the tensor cores take bf16 parts. A bf16 q, k, v is one part; an f16 one splits
-// into two exactly and an f32 one into three (8 bits each, 24 in all). Scores and the state
-// as an operand keep two parts (16 bits) for 16-bit outputs and three for f32; the decayed
-// keys keep three always, because they are summed into the f32 state. Products of parts
-// below the last kept bit are left out. Sums, statistics and the state itself are f32.
+// Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; an
+// f32 one splits into three bf16 parts (8 bits each, 24 in all). Scores and the state as an
+// operand keep two parts for 16-bit types (16 bits in bf16, 22 in f16) and three for f32. The
+// decayed keys are summed into the f32 state, so they keep f32's bits whatever the type:
+// three bf16 parts or two f16 ones. f16 parts need their values in f16's range: scores and
+// states are scaled by a power of two for each row, decayed keys for each chunk. Products of
+// parts below the last kept bit are left out. Sums, statistics and the state are f32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "linattn.cuh"
 #include "tc.cuh"
@@ -42,7 +46,7 @@ struct Plan {
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
   static constexpr uint32_t P = KT + 3 * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
-  static constexpr uint32_t BYTES = MISC + 4096;  // bf16: 112,640 bytes and 1,024 of slack, two CTAs an SM
+  static constexpr uint32_t BYTES = MISC + 5760;  // NP 1: 114,304 bytes and 1,024 of slack, two CTAs an SM
   // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
   // their place once O2 is done where there are two of them (a thread's columns of A are its
   // columns of the parts).
@@ -59,7 +63,8 @@ struct Decays {
   float ghi, glo;    // sum over the chunk without resets
   int reset;         // whether the chunk forgets
   int mild;          // no resets, and every exp(G_t) within 2^-80 .. 2^20
-  int pad[3];
+  float wmax;        // largest w
+  int pad[2];
 };
 struct Misc {
   Decays d[2];       // of this chunk and the next
@@ -67,12 +72,16 @@ struct Misc {
   uint64_t qk, qs, end;             // products are done
   uint32_t tmem;
   int scratch[4 + 16];
+  // f16: largest magnitudes on the way to the scales, and the scores' inverse scales
+  alignas(16) float pinv[CH];
+  float kmax[8], smax[2][128], pmax[2][32];
 };
-static_assert(sizeof(Misc) <= 4096, "misc");
+static_assert(sizeof(Misc) <= 5760, "misc");
 
-// bf16 K-major (bit 0) or MN-major (1) operands, f32 accumulator, shape M x N.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int ta, int tb) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)ta << 15 | (uint32_t)tb << 16 | (uint32_t)(N >> 3) << 17 |
+// bf16 (or f16) operands, K-major (0) or MN-major (1), f32 accumulator, shape M x N.
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int ta, int tb) {
+  return 1u << 4 | (F16 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)ta << 15 | (uint32_t)tb << 16 | (uint32_t)(N >> 3) << 17 |
          (uint32_t)(M >> 4) << 24;
 }
 __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
@@ -121,10 +130,12 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
       : "memory");
 }
 // 64 tokens of one head (zeros past the tensor's end, and for columns past the head's width).
-__device__ __forceinline__ void tma_load_tile(uint8_t* dst, const CUtensorMap* map, int head, int t0, uint64_t* bar) {
-  mbar_arrive_expect_tx(bar, TILE);
+// Columns 64 .. 127 only for heads that have some.
+__device__ __forceinline__ void tma_load_tile(uint8_t* dst, const CUtensorMap* map, int dim, int head, int t0,
+                                              uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, dim > 64 ? TILE : TILE / 2);
   tma_load(dst, map, 0, head, t0, bar);
-  tma_load(dst + TILE / 2, map, 64, head, t0, bar);
+  if (dim > 64) tma_load(dst + TILE / 2, map, 64, head, t0, bar);
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
@@ -135,23 +146,34 @@ __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.com
 __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Two f32 values as n bf16 parts each, packed in pairs (low half: x0); the parts sum to the
-// value to 8 n bits.
-template <int n>
+// A pair of 16-bit values (low half first) as f32.
+template <bool F16>
+__device__ __forceinline__ float2 unpack(uint32_t u) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// Two f32 values as n parts each, packed in pairs; the parts sum to the value to 8 n (f16: 11 n) bits.
+template <int n, bool F16 = false>
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t* out) {
 #pragma unroll
   for (int p = 0; p < n; ++p) {
     uint32_t h;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
     out[p] = h;
     if (p + 1 < n) {
-      x0 -= __uint_as_float(h << 16);
-      x1 -= __uint_as_float(h & 0xffff0000u);
+      const float2 f = unpack<F16>(h);
+      x0 -= f.x;
+      x1 -= f.y;
     }
   }
 }
-__device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// The power of two that brings a magnitude up to mx (0 and what is not finite included) to
+// 2^14 .. 2^15, inside f16, and its inverse; both normal.
+__device__ __forceinline__ float2 f16_scale(float mx) {
+  const int e = min(max((int)(__float_as_uint(mx) >> 23), 16), 254);
+  return make_float2(__uint_as_float((uint32_t)(268 - e) << 23), __uint_as_float((uint32_t)(e - 14) << 23));
+}
 // Tiles written by threads are kept as [column / 8][row][8 columns]: 8 rows x 16 bytes are one core matrix, so the
 // same bytes serve as a K-major operand (columns along K: core matrices 1024 bytes apart
 // along K, 128 along rows) and as an MN-major one (rows along K: 128 along K, 1024 along columns).
@@ -191,10 +213,7 @@ struct Loader {
         uint32_t u[4][NP];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float2 x;
-          if constexpr (sizeof(T) == 4) x = make_float2(__uint_as_float(r[i][2 * j]), __uint_as_float(r[i][2 * j + 1]));
-          else x = __half22float2(*reinterpret_cast<const __half2*>(&r[i][j]));
-          split_pair<NP>(x.x, x.y, u[j]);
+          split_pair<NP>(__uint_as_float(r[i][2 * j]), __uint_as_float(r[i][2 * j + 1]), u[j]);
         }
         uint8_t* d = dst + piece(i * 4 + (lane >> 3), row);
 #pragma unroll
@@ -211,7 +230,7 @@ __device__ __forceinline__ uint32_t tile_piece(int kc, int row) {
   return piece(kc, row);
 }
 // Eight values of a piece, the parts added up (exact: they do not overlap).
-template <int NP>
+template <int NP, bool F16>
 __device__ __forceinline__ void read_piece(const uint8_t* p, float (&x)[8]) {
 #pragma unroll
   for (int q = NP - 1; q >= 0; --q) {
@@ -219,17 +238,17 @@ __device__ __forceinline__ void read_piece(const uint8_t* p, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      x[2 * j] = lo_f32(w[j]) + (q == NP - 1 ? 0.f : x[2 * j]);
-      x[2 * j + 1] = hi_f32(w[j]) + (q == NP - 1 ? 0.f : x[2 * j + 1]);
+      const float2 f = unpack<F16>(w[j]);
+      x[2 * j] = f.x + (q == NP - 1 ? 0.f : x[2 * j]);
+      x[2 * j + 1] = f.y + (q == NP - 1 ? 0.f : x[2 * j + 1]);
     }
   }
 }
-
 // The products of parts i < NA of one operand and j < NB of the other with i + j <= LIM, each
-// in KS steps of 16 along K: the smallest first, because the tensor core's accumulator
+// in the first `ks` of KS steps of 16 along K: the smallest first, because the tensor core's accumulator
 // loses up to a last bit with every step, of what it holds by then.
 template <int NA, int NB, int LIM, int KS, typename F>
-__device__ __forceinline__ void each_product(F f) {
+__device__ __forceinline__ void each_product(int ks, F f) {
   bool first = true;
 #pragma unroll
   for (int sum = LIM; sum >= 0; --sum)
@@ -239,7 +258,10 @@ __device__ __forceinline__ void each_product(F f) {
       for (int j = 0; j < NB; ++j)
         if (i + j == sum)
 #pragma unroll
-          for (int s = 0; s < KS; ++s, first = false) f(i, j, s, first);
+          for (int s = 0; s < KS; ++s) {
+            if (s < ks) f(i, j, s, first);
+            first = false;
+          }
 }
 
 // The chunk's decays, by one warp (lane: tokens 2 lane, 2 lane + 1). Sums are carried as an
@@ -291,16 +313,20 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
   const bool ok = fminf(ph, ch) > -80.f && fmaxf(ph, ch) < 20.f && ph == ph && ch == ch;
   const bool mild = __all_sync(0xffffffffu, ok) && er == 0;
   const float gh[2] = {ph, ch}, gl[2] = {pl, cl};
+  float wm = 0.f;
   const int gr[2] = {pr, cr};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int t = 2 * lane + j;
     m->g[t] = make_float4(gh[j], gl[j], (float)gr[j], expf(raw[j]));
     m->w[t] = gr[j] == er ? ex2((eh - gh[j]) + (el - gl[j])) : 0.f;
+    wm = fmaxf(wm, m->w[t]);
     m->eg[t] = gr[j] == 0 ? ex2(gh[j] + gl[j]) : 0.f;
     m->ieg[t] = ex2(-(gh[j] + gl[j]));
   }
+  wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wm)));  // of non-negative numbers
   if (lane == 0) {
+    m->wmax = wm;
     m->lam = er == 0 ? ex2(eh + el) : 0.f;
     m->ghi = eh;
     m->glo = el;
@@ -310,23 +336,27 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
 }
 
 struct Maps {
-  CUtensorMap q, k, v, o;  // bf16 only
+  CUtensorMap q, k, v, o;  // 16-bit types only
 };
 
 // MODE 0: the state that a unit's tokens alone leave, and its decay, into the workspace.
 // MODE 1: the outputs, from the state before the unit; the sequence's last unit stores it.
-// `wd`: decays [states][H], `wst`: states [states][H][dk][dv]; seg: tokens of a unit.
+// `wd`: decays [states][H], `wst`: states [states][H][dk][dv]; seg: tokens of a unit. WIDE: keys
+// of more than 112 values, whose eight steps along K are then fixed (237 against 259 us for
+// 16,384 tokens x 32 heads of 128).
 //
 // Eight warps; thread 96 (warp 3, which has no scores to mask) also issues the products and
 // the TMA copies, each as soon as its inputs are ready and its target is free:
 //   QK | QS, KV while the scores are masked | PV; the next k after QK, q after QS, v after
 //   the outputs, which are turned in v's place, have left it.
 // Two bf16 CTAs share an SM, so one's products run beside the other's arithmetic.
-template <typename T, int NP, int MODE>
+template <typename T, int NP, int MODE, bool WIDE>
 __global__ void __launch_bounds__(256, NP == 1 ? 2 : 1)
 lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
   using L = Plan<NP>;
+  constexpr bool F16 = std::is_same<T, __half>::value;
   constexpr int NPP = L::NPP, LIM = NP == 3 ? 2 : 1;  // products of parts i, j with i + j <= LIM
+  constexpr int KP = F16 ? 2 : 3;                     // parts of the decayed keys
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
@@ -363,7 +393,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = m->tmem, tlane = tm + ((uint32_t)quarter * 32u << 16);
-  const int hq = h / a.rep;
+  const int hq = h / a.rep, ks = WIDE ? D / 16 : (a.dk + 15) / 16;  // steps of 16 along the keys' width
+  const bool cols = WIDE || wg * 64 < a.dk;                 // whether this thread's half of S^T has columns
   const T* q = static_cast<const T*>(a.q) + (int64_t)hq * a.dk;
   const T* k = static_cast<const T*>(a.k) + (int64_t)hq * a.dk;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
@@ -372,9 +403,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   float* mine = wst + ((int64_t)(un.slot0 + un.i) * a.H + h) * sz;  // sequences of several units
 
   if (NP == 1 && issuer && begin < end) {
-    tma_load_tile(sm + L::K, &maps.k, hq, begin, &m->full_k);
-    if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, hq, begin, &m->full_q);
-    tma_load_tile(sm + L::V, &maps.v, h, begin, &m->full_v);
+    tma_load_tile(sm + L::K, &maps.k, a.dk, hq, begin, &m->full_k);
+    if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, begin, &m->full_q);
+    tma_load_tile(sm + L::V, &maps.v, a.dv, h, begin, &m->full_v);
   }
   Loader<T, NP> lq, lk, lv;
   if (NP > 1 && begin < end) {
@@ -395,30 +426,50 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     for (int j = 0; j < 64; ++j)
       S[j] = !zero && row < a.dv && wg * 64 + j < a.dk ? from[(wg * 64 + j) * a.dv + row] : 0.f;
   }
+  float sinv = 1.f;  // f16: inverse scale of this row of the operand
   auto put_state = [&]() {  // the state's parts as an operand in tensor memory
+    float sc = 1.f;
+    if constexpr (F16) {
+      float mx = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t u[NPP][16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        uint32_t s[NPP];
-        split_pair<NPP>(S[c * 32 + 2 * j], S[c * 32 + 2 * j + 1], s);
-#pragma unroll
-        for (int p = 0; p < NPP; ++p) u[p][j] = s[p];
-      }
-#pragma unroll
-      for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + (wg * NPP + p) * 32 + c * 16, u[p]);
+      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, fabsf(S[j]));
+      m->smax[wg][row] = mx;
+      __syncthreads();
+      const float2 f = f16_scale(fmaxf(mx, m->smax[wg ^ 1][row]));
+      sc = f.x;
+      sinv = f.y;
     }
-    tmem_st_wait();
+    if (cols) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t u[NPP][16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          uint32_t s[NPP];
+          split_pair<NPP, F16>(S[c * 32 + 2 * j] * sc, S[c * 32 + 2 * j + 1] * sc, s);
+#pragma unroll
+          for (int p = 0; p < NPP; ++p) u[p][j] = s[p];
+        }
+#pragma unroll
+        for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + (wg * NPP + p) * 32 + c * 16, u[p]);
+      }
+      tmem_st_wait();
+    }
   };
-  auto add_state = [&](float lam) {  // S = lam S + A
+  auto add_state = [&](float lam, float ainv) {  // S = lam S + A
+    if (cols) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t r[16];
-      tmem_ld16(tlane + L::T_A + wg * 64 + c * 16, r);
-      tmem_ld_wait();
+      for (int c = 0; c < 4; ++c) {
+        if (wg * 4 + c >= ks) break;  // columns that A does not have
+        uint32_t r[16];
+        tmem_ld16(tlane + L::T_A + wg * 64 + c * 16, r);
+        tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) S[c * 16 + j] = fmaf(lam, S[c * 16 + j], __uint_as_float(r[j]));
+        for (int j = 0; j < 16; ++j) {
+          const float x = __uint_as_float(r[j]);
+          S[c * 16 + j] = fmaf(lam, S[c * 16 + j], F16 ? x * ainv : x);
+        }
+      }
     }
   };
   // A masked product with an infinity or a NaN is a NaN, which would reach the chunk's earlier
@@ -472,28 +523,49 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     if (MODE == 1 && issuer) {
       if (NP == 1) ok = mbar_wait(&m->full_q, ph) && mbar_wait(&m->full_k, ph) && ok;
       tc_fence_after_sync();
-      each_product<NP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+      each_product<NP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
         mma_f16(tm + L::T_O1, desc_k<NP>(sm + L::Q + i * TILE, s), desc_k<NP>(sm + L::K + j * TILE, s),
-                idesc_bf16(128, CH, 0, 0), !first);
+                idesc<F16>(128, CH, 0, 0), !first);
       });
       mma_commit(&m->qk);
     }
     __syncwarp();
-    // ---- the decayed keys, three parts ------------------------------------------------
+    // ---- the decayed keys ---------------------------------------------------------------
     if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
-    if (NP == 1 && t0 == begin) __syncthreads();  // the first decays
+    if (NP == 1 && !F16 && t0 == begin) __syncthreads();  // the first decays
+    float2 kscale = make_float2(1.f, 1.f);
+    if constexpr (F16) {
+      uint32_t mx = 0;  // as packed f16 bits, of which the unsigned order is that of magnitudes
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
+        if (r < n && kc < 2 * ks) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sm + L::K + tile_piece<NP>(kc, r));
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                     __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        }
+      }
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      if (lane == 0) m->kmax[warp] = __half2float(__ushort_as_half((unsigned short)mx));
+      __syncthreads();  // also: the first decays
+      float km = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) km = fmaxf(km, m->kmax[i]);
+      kscale = f16_scale(km * d->wmax);
+    }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
-      const float w = d->w[r];
+      if (i * 4 >= 2 * ks) break;
+      const float w = d->w[r] * kscale.x;
       float x[8];
-      read_piece<NP>(sm + L::K + tile_piece<NP>(kc, r), x);
-      uint32_t u[4][3];
+      read_piece<NP, F16>(sm + L::K + tile_piece<NP>(kc, r), x);
+      uint32_t u[4][KP];
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // rows past the chunk's tokens are other sequences' or none
-        split_pair<3>(r < n ? x[2 * j] * w : 0.f, r < n ? x[2 * j + 1] * w : 0.f, u[j]);
+        split_pair<KP, F16>(r < n ? x[2 * j] * w : 0.f, r < n ? x[2 * j + 1] * w : 0.f, u[j]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
+      for (int p = 0; p < KP; ++p)
         *reinterpret_cast<uint4*>(sm + L::KT + p * TILE + piece(kc, r)) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
     }
     if (NP == 1 && n < CH) {
@@ -525,24 +597,24 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     // ---- the state's share, and what the chunk adds to the state -------------------------
     if (issuer) {
       if (MODE == 1) {
-        each_product<NPP, NP, LIM, D / 16>([&](int i, int j, int s, bool first) {
+        each_product<NPP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
           mma_ts(tm + L::T_O2, tm + L::T_S + (s / 4 * NPP + i) * 32 + s % 4 * 8, desc_k<NP>(sm + L::Q + j * TILE, s),
-                 idesc_bf16(128, CH, 0, 0), !first);
+                 idesc<F16>(128, CH, 0, 0), !first);
         });
         mma_commit(&m->qs);
         ok = mbar_wait(&m->qk, ph) && ok;
       }
-      if (NP == 1 && more) tma_load_tile(sm + L::K, &maps.k, hq, t0 + CH, &m->full_k);
+      if (NP == 1 && more) tma_load_tile(sm + L::K, &maps.k, a.dk, hq, t0 + CH, &m->full_k);
       if (MODE == 1) ok = mbar_wait(&m->qs, ph) && ok;
       if (NP == 1) ok = mbar_wait(&m->full_v, ph) && ok;
       tc_fence_after_sync();
-      each_product<NP, 3, 2, CH / 16>([&](int i, int j, int s, bool first) {
+      each_product<NP, KP, KP - 1, CH / 16>(CH / 16, [&](int i, int j, int s, bool first) {
         mma_f16(tm + L::T_A, desc_mn<NP>(tv + i * TILE, s), smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024),
-                idesc_bf16(128, D, 1, 1), !first);
+                idesc<F16>(128, 16 * ks, 1, 1), !first);
       });
       if (NP == 1 && more) {
-        if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, hq, t0 + CH, &m->full_q);
-        else tma_load_tile(sm + (ph ? L::V : L::Q), &maps.v, h, t0 + CH, &m->full_v);
+        if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, t0 + CH, &m->full_q);
+        else tma_load_tile(sm + (ph ? L::V : L::Q), &maps.v, a.dv, h, t0 + CH, &m->full_v);
       }
       if (MODE == 0) mma_commit(&m->end);
     }
@@ -555,10 +627,12 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       tc_fence_after_sync();
       const float4 gt = d->g[row];
       const float et = d->eg[row];
+      uint32_t sc[2][16];
+      float mx = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int step = wg * 2 + c;  // of the product over s
-        uint32_t s[16];
+        uint32_t (&s)[16] = sc[c];
         tmem_ld16(tlane + L::T_O1 + step * 16, s);
         tmem_ld_wait();
         // exp(G_t - G_s): where the chunk's decays are mild, as a product of two factors (16-bit
@@ -581,13 +655,33 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
           }
         }
 #pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          s[j] = step * 16 + j <= row ? s[j] : 0u;
+          if (F16) mx = fmaxf(mx, fabsf(__uint_as_float(s[j])));
+        }
+      }
+      float rs = 1.f;
+      if constexpr (F16) {  // rows 32 .. 63 are two threads'
+        if (quarter == 1) {
+          m->pmax[wg][lane] = mx;
+          asm volatile("bar.sync 2, 64;" ::: "memory");
+          mx = fmaxf(mx, m->pmax[wg ^ 1][lane]);
+        }
+        const float2 f = f16_scale(mx);
+        rs = f.x;
+        if (wg == 0) m->pinv[row] = f.y;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int step = wg * 2 + c;
+#pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t u[4][NPP];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c0 = e * 8 + 2 * j;
-            split_pair<NPP>(step * 16 + c0 <= row ? __uint_as_float(s[c0]) : 0.f,
-                            step * 16 + c0 + 1 <= row ? __uint_as_float(s[c0 + 1]) : 0.f, u[j]);
+            const float p0 = __uint_as_float(sc[c][c0]), p1 = __uint_as_float(sc[c][c0 + 1]);
+            split_pair<NPP, F16>(F16 ? p0 * rs : p0, F16 ? p1 * rs : p1, u[j]);
           }
           if (row >= step * 16) {
 #pragma unroll
@@ -605,9 +699,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       asm volatile("bar.sync 1, 128;" ::: "memory");
       tc_fence_after_sync();
       if (issuer) {
-        each_product<NP, NPP, LIM, CH / 16>([&](int i, int j, int s, bool first) {
+        each_product<NP, NPP, LIM, CH / 16>(CH / 16, [&](int i, int j, int s, bool first) {
           mma_f16(tm + L::T_O1 + s * 16, desc_mn<NP>(tv + i * TILE, s),
-                  smem_desc(sm + L::P + j * PTILE + p_base(s), p_pitch(s), 128), idesc_bf16(128, CH - 16 * s, 1, 0),
+                  smem_desc(sm + L::P + j * PTILE + p_base(s), p_pitch(s), 128), idesc<F16>(128, CH - 16 * s, 1, 0),
                   !first);
         });
         mma_commit(&m->end);
@@ -617,7 +711,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     ok = mbar_wait(&m->end, ph) && ok;
     tc_fence_after_sync();
     if (MODE == 0) {
-      add_state(d->lam);
+      add_state(d->lam, kscale.y);
       lk.put(sm + L::K);
       if (NP == 1) __syncthreads();  // the next decays are there
       continue;
@@ -639,10 +733,16 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
         const int t = wg * 32 + c * 16 + j;
         const float4 e = *reinterpret_cast<const float4*>(&d->eg[t]);
         const float ev[4] = {e.x, e.y, e.z, e.w};
+        float pv[4] = {1.f, 1.f, 1.f, 1.f};
+        if (F16) {
+          const float4 p = *reinterpret_cast<const float4*>(&m->pinv[t]);
+          pv[0] = p.x, pv[1] = p.y, pv[2] = p.z, pv[3] = p.w;
+        }
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const float x = fmaf(ev[f], __uint_as_float(o2[j + f]), __uint_as_float(o1[j + f])) * a.scale;
-          if (t + f < n) bad = fmaf(x, 0.f, bad);
+          const float y1 = __uint_as_float(o1[j + f]), y2 = __uint_as_float(o2[j + f]);
+          const float x = (F16 ? fmaf(ev[f], y2 * sinv, y1 * pv[f]) : fmaf(ev[f], y2, y1)) * a.scale;
+          if (t + f < n && row < a.dv) bad = fmaf(x, 0.f, bad);
           stage[(row / SW) * CH * SW + (t + f) * SW + row % SW] = from_f32<T>(x);
         }
       }
@@ -671,12 +771,12 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
                 *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(stage) + i * 16);
         }
       }
-      add_state(d->lam);
+      add_state(d->lam, kscale.y);
     }
     put_state();
     if (NP == 1 && issuer) {
       store_wait_read();
-      if (more) tma_load_tile(sm + L::V, &maps.v, h, t0 + CH, &m->full_v);
+      if (more) tma_load_tile(sm + L::V, &maps.v, a.dv, h, t0 + CH, &m->full_v);
     }
     __syncwarp();
   }
@@ -743,7 +843,7 @@ cudaError_t launch(K kern, dim3 grid, int smem, bool pdl, cudaStream_t st, Args.
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// A [tokens][heads][dim] bf16 tensor in boxes of 64 tokens x 64 columns of one head, rows of
+// A [tokens][heads][dim] tensor of 16-bit values in boxes of 64 tokens x 64 columns of one head, rows of
 // 128 bytes, in the 128-byte swizzle for operands and as they are for outputs.
 cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int tokens, int64_t stride, bool swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -765,7 +865,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int NP>
+template <typename T, int NP, bool WIDE>
 cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream_t st) {
   const LinattnSplit sp = linattn_split(a.N, a.B, a.H, a.dk, a.dv);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws);
@@ -784,22 +884,26 @@ cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
   const bool several = a.offsets ? sp.units > a.B : a.seq_len > sp.seg;
   if (several) {
-    e = launch(lin_chunk<T, NP, 0>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
+    e = launch(lin_chunk<T, NP, 0, WIDE>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
     if (e != cudaSuccess) return e;
     const dim3 jgrid((unsigned)sp.units, (unsigned)a.H, (unsigned)((a.dk * a.dv + 1023) / 1024));
     e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
+  return launch(lin_chunk<T, NP, 1, WIDE>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
 }
 
 }  // namespace
 
 cudaError_t linattn_chunk_launch(const LinattnArgs& a, int type, void* ws, bool pdl, cudaStream_t st) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  if (type == MOE_F32) return chunk_launch<float, 3>(a, w, pdl, st);
-  if (type == MOE_F16) return chunk_launch<__half, 2>(a, w, pdl, st);
-  return chunk_launch<__nv_bfloat16, 1>(a, w, pdl, st);
+  const bool wide = a.dk > 112;
+  if (type == MOE_F32)
+    return wide ? chunk_launch<float, 3, true>(a, w, pdl, st) : chunk_launch<float, 3, false>(a, w, pdl, st);
+  if (type == MOE_F16)
+    return wide ? chunk_launch<__half, 1, true>(a, w, pdl, st) : chunk_launch<__half, 1, false>(a, w, pdl, st);
+  return wide ? chunk_launch<__nv_bfloat16, 1, true>(a, w, pdl, st)
+              : chunk_launch<__nv_bfloat16, 1, false>(a, w, pdl, st);
 }
 
 }  // namespace moe
