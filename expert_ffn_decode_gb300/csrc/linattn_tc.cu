@@ -101,6 +101,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of a converged warp, the same one every time. Branching on it (and on a warp index
+// the compiler knows to be uniform) keeps the operands of what follows in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -345,7 +352,7 @@ struct Maps {
 // of more than 112 values, whose eight steps along K are then fixed (237 against 259 us for
 // 16,384 tokens x 32 heads of 128).
 //
-// Eight warps; thread 96 (warp 3, which has no scores to mask) also issues the products and
+// Eight warps; one lane of warp 3, which has no scores to mask, also issues the products and
 // the TMA copies, each as soon as its inputs are ready and its target is free:
 //   QK | QS, KV while the scores are masked | PV; the next k after QK, q after QS, v after
 //   the outputs, which are turned in v's place, have left it.
@@ -361,7 +368,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   uint8_t* sm = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, quarter = warp & 3;
-  const bool issuer = tid == 96;
+  const bool iwarp = __shfl_sync(0xffffffffu, warp, 0) == 3;  // whose elected lane issues
   const int h = blockIdx.y, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
   pdl_wait_prior_grids();
   const Unit un = find_unit(a, seg, n_ws, blockIdx.x, m->scratch);
@@ -392,7 +399,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tm = m->tmem, tlane = tm + ((uint32_t)quarter * 32u << 16);
+  const uint32_t tm = __shfl_sync(0xffffffffu, m->tmem, 0), tlane = tm + ((uint32_t)quarter * 32u << 16);
   const int hq = h / a.rep, ks = WIDE ? D / 16 : (a.dk + 15) / 16;  // steps of 16 along the keys' width
   const bool cols = WIDE || wg * 64 < a.dk;                 // whether this thread's half of S^T has columns
   const T* q = static_cast<const T*>(a.q) + (int64_t)hq * a.dk;
@@ -402,7 +409,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   float* pool = a.state + ((int64_t)slot * a.H + h) * sz;
   float* mine = wst + ((int64_t)(un.slot0 + un.i) * a.H + h) * sz;  // sequences of several units
 
-  if (NP == 1 && issuer && begin < end) {
+  if (NP == 1 && begin < end && iwarp && elect_one()) {
     tma_load_tile(sm + L::K, &maps.k, a.dk, hq, begin, &m->full_k);
     if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, begin, &m->full_q);
     tma_load_tile(sm + L::V, &maps.v, a.dv, h, begin, &m->full_v);
@@ -520,7 +527,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       lv.fetch(v, a.vs, t0, n, a.dv);
     }
     // ---- scores ----------------------------------------------------------------------
-    if (MODE == 1 && issuer) {
+    if (MODE == 1 && iwarp && elect_one()) {
       if (NP == 1) ok = mbar_wait(&m->full_q, ph) && mbar_wait(&m->full_k, ph) && ok;
       tc_fence_after_sync();
       each_product<NP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
@@ -595,7 +602,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     }
     if (warp == 7 && more) chunk_decays(a, h, t0 + CH, min(CH, end - t0 - CH), &m->d[ph ^ 1]);
     // ---- the state's share, and what the chunk adds to the state -------------------------
-    if (issuer) {
+    if (iwarp && elect_one()) {
       if (MODE == 1) {
         each_product<NPP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
           mma_ts(tm + L::T_O2, tm + L::T_S + (s / 4 * NPP + i) * 32 + s % 4 * 8, desc_k<NP>(sm + L::Q + j * TILE, s),
@@ -695,10 +702,10 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       tc_fence_before_sync();
       asm volatile("bar.arrive 1, 128;" ::: "memory");  // three warps of scores and the issuer's
     }
-    if (MODE == 1 && warp == 3) {
+    if (MODE == 1 && iwarp) {
       asm volatile("bar.sync 1, 128;" ::: "memory");
       tc_fence_after_sync();
-      if (issuer) {
+      if (elect_one()) {
         each_product<NP, NPP, LIM, CH / 16>(CH / 16, [&](int i, int j, int s, bool first) {
           mma_f16(tm + L::T_O1 + s * 16, desc_mn<NP>(tv + i * TILE, s),
                   smem_desc(sm + L::P + j * PTILE + p_base(s), p_pitch(s), 128), idesc<F16>(128, CH - 16 * s, 1, 0),
@@ -757,7 +764,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       token_by_token(t0, n, d);
     } else {
       if (NP == 1 && n == CH) {
-        if (issuer) {
+        if (iwarp && elect_one()) {
           tma_store(&maps.o, stage, 0, h, t0);
           if (a.dv > 64) tma_store(&maps.o, stage + CH * SW, 64, h, t0);
           store_commit();
@@ -774,13 +781,13 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       add_state(d->lam, kscale.y);
     }
     put_state();
-    if (NP == 1 && issuer) {
+    if (NP == 1 && iwarp && elect_one()) {
       store_wait_read();
       if (more) tma_load_tile(sm + L::V, &maps.v, a.dv, h, t0 + CH, &m->full_v);
     }
     __syncwarp();
   }
-  if (NP == 1 && issuer && begin < end) {  // no copy is left in flight, whatever ended the loop
+  if (NP == 1 && begin < end && iwarp && elect_one()) {  // no copy is left in flight, whatever ended the loop
     const uint32_t p = ok ? ph ^ 1 : ph;
     ok = mbar_wait(&m->full_k, p) && ok;
     if (MODE == 1) ok = mbar_wait(&m->full_q, p) && ok;
@@ -795,7 +802,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       if (row < a.dv && wg * 64 + j < a.dk) to[(wg * 64 + j) * a.dv + row] = S[j];
   }
   if (MODE == 0 && tid == 0) wd[(int64_t)(un.slot0 + un.i) * a.H + h] = resets ? 0.f : ex2(sum_hi + sum_lo);
-  if (NP == 1 && MODE == 1 && issuer) store_wait_all();
+  if (NP == 1 && MODE == 1 && iwarp && elect_one()) store_wait_all();
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tm, L::T_COLS);
