@@ -354,8 +354,9 @@ struct Maps {
 //
 // Eight warps; one lane of warp 3, which has no scores to mask, also issues the products and
 // the TMA copies, each as soon as its inputs are ready and its target is free:
-//   QK | QS, KV while the scores are masked | PV; the next k after QK, q after QS, v after
-//   the outputs, which are turned in v's place, have left it.
+//   QS, KV while the scores are masked | PV | the next chunk's QK while the state is updated;
+//   the next k after QK, q after QS, v after the outputs, which are turned in v's place, have
+//   left it.
 // Two bf16 CTAs share an SM, so one's products run beside the other's arithmetic.
 template <typename T, int NP, int MODE, bool WIDE>
 __global__ void __launch_bounds__(256, NP == 1 ? 2 : 1)
@@ -513,6 +514,18 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 
   uint32_t ph = 0;  // parity of this chunk's phases
   bool ok = true;
+  auto issue_scores = [&](uint32_t p) {
+    if (MODE == 1 && iwarp && elect_one()) {
+      if (NP == 1) ok = mbar_wait(&m->full_q, p) && mbar_wait(&m->full_k, p) && ok;
+      tc_fence_after_sync();
+      each_product<NP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
+        mma_f16(tm + L::T_O1, desc_k<NP>(sm + L::Q + i * TILE, s), desc_k<NP>(sm + L::K + j * TILE, s),
+                idesc<F16>(128, CH, 0, 0), !first);
+      });
+      mma_commit(&m->qk);
+    }
+    __syncwarp();
+  };
   float sum_hi = 0.f, sum_lo = 0.f;
   int resets = 0;
   for (int t0 = begin; t0 < end; t0 += CH, ph ^= 1) {
@@ -526,17 +539,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
       lv.fetch(v, a.vs, t0, n, a.dv);
     }
-    // ---- scores ----------------------------------------------------------------------
-    if (MODE == 1 && iwarp && elect_one()) {
-      if (NP == 1) ok = mbar_wait(&m->full_q, ph) && mbar_wait(&m->full_k, ph) && ok;
-      tc_fence_after_sync();
-      each_product<NP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
-        mma_f16(tm + L::T_O1, desc_k<NP>(sm + L::Q + i * TILE, s), desc_k<NP>(sm + L::K + j * TILE, s),
-                idesc<F16>(128, CH, 0, 0), !first);
-      });
-      mma_commit(&m->qk);
-    }
-    __syncwarp();
+    if (t0 == begin) issue_scores(ph);
     // ---- the decayed keys ---------------------------------------------------------------
     if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
     if (NP == 1 && !F16 && t0 == begin) __syncthreads();  // the first decays
@@ -613,16 +616,15 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       }
       if (NP == 1 && more) tma_load_tile(sm + L::K, &maps.k, a.dk, hq, t0 + CH, &m->full_k);
       if (MODE == 1) ok = mbar_wait(&m->qs, ph) && ok;
+      if (NP == 1 && MODE == 1 && more) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, t0 + CH, &m->full_q);
       if (NP == 1) ok = mbar_wait(&m->full_v, ph) && ok;
+      // (this chunk's v has landed, so its barrier is free for the next one's)
+      if (NP == 1 && MODE == 0 && more) tma_load_tile(sm + (ph ? L::V : L::Q), &maps.v, a.dv, h, t0 + CH, &m->full_v);
       tc_fence_after_sync();
       each_product<NP, KP, KP - 1, CH / 16>(CH / 16, [&](int i, int j, int s, bool first) {
         mma_f16(tm + L::T_A, desc_mn<NP>(tv + i * TILE, s), smem_desc(sm + L::KT + j * TILE + s * 256, 128, 1024),
                 idesc<F16>(128, 16 * ks, 1, 1), !first);
       });
-      if (NP == 1 && more) {
-        if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, t0 + CH, &m->full_q);
-        else tma_load_tile(sm + (ph ? L::V : L::Q), &maps.v, a.dv, h, t0 + CH, &m->full_v);
-      }
       if (MODE == 0) mma_commit(&m->end);
     }
     __syncwarp();
@@ -760,6 +762,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     tc_fence_before_sync();
     const bool redo = __syncthreads_or(bad != 0.f);  // a sum of zeros unless a value is not finite
     tc_fence_after_sync();
+    // the next chunk's scores may take O1's place: its q and k have come meanwhile
+    if (more) issue_scores(ph ^ 1);
     if (redo) {
       token_by_token(t0, n, d);
     } else {
