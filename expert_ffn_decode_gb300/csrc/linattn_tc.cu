@@ -57,7 +57,7 @@ struct Plan {
 struct Decays {
   float4 g[CH];      // G_t in powers of two: sum's high and low part, resets so far, exp(g_t)
   float w[CH];       // exp(G_63 - G_s)
-  float eg[CH];      // exp(G_t)
+  float eg[CH];      // scale * exp(G_t)
   float ieg[CH];     // exp(-G_t), where `mild`
   float lam;         // exp(G_63)
   float ghi, glo;    // sum over the chunk without resets
@@ -328,7 +328,7 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
     m->g[t] = make_float4(gh[j], gl[j], (float)gr[j], expf(raw[j]));
     m->w[t] = gr[j] == er ? ex2((eh - gh[j]) + (el - gl[j])) : 0.f;
     wm = fmaxf(wm, m->w[t]);
-    m->eg[t] = gr[j] == 0 ? ex2(gh[j] + gl[j]) : 0.f;
+    m->eg[t] = gr[j] == 0 ? ex2(gh[j] + gl[j]) * a.scale : 0.f;
     m->ieg[t] = ex2(-(gh[j] + gl[j]));
   }
   wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wm)));  // of non-negative numbers
@@ -570,10 +570,13 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       const float w = d->w[r] * kscale.x;
       float x[8];
       read_piece<NP, F16>(sm + L::K + tile_piece<NP>(kc, r), x);
+      if (n < CH && r >= n) {  // rows past the chunk's tokens are other sequences' or none
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = 0.f;
+      }
       uint32_t u[4][KP];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)  // rows past the chunk's tokens are other sequences' or none
-        split_pair<KP, F16>(r < n ? x[2 * j] * w : 0.f, r < n ? x[2 * j + 1] * w : 0.f, u[j]);
+      for (int j = 0; j < 4; ++j) split_pair<KP, F16>(x[2 * j] * w, x[2 * j + 1] * w, u[j]);
 #pragma unroll
       for (int p = 0; p < KP; ++p)
         *reinterpret_cast<uint4*>(sm + L::KT + p * TILE + piece(kc, r)) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
@@ -660,13 +663,16 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
           for (int j = 0; j < 16; ++j) {
             const float4 gs = d->g[step * 16 + j];
             const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
-            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * x) : 0u;
+            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * x * a.scale) : 0u;
           }
         }
+        if (wg == quarter) {  // (rows 32 .. 63 see all of the first 32 columns)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          s[j] = step * 16 + j <= row ? s[j] : 0u;
-          if (F16) mx = fmaxf(mx, fabsf(__uint_as_float(s[j])));
+          for (int j = 0; j < 16; ++j) s[j] = step * 16 + j <= row ? s[j] : 0u;
+        }
+        if (F16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(__uint_as_float(s[j])));
         }
       }
       float rs = 1.f;
@@ -750,8 +756,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const float y1 = __uint_as_float(o1[j + f]), y2 = __uint_as_float(o2[j + f]);
-          const float x = (F16 ? fmaf(ev[f], y2 * sinv, y1 * pv[f]) : fmaf(ev[f], y2, y1)) * a.scale;
-          if (t + f < n && row < a.dv) bad = fmaf(x, 0.f, bad);
+          const float x = F16 ? fmaf(ev[f], y2 * sinv, y1 * pv[f]) : fmaf(ev[f], y2, y1);
+          bad = fmaf(x, 0.f, bad);
           stage[(row / SW) * CH * SW + (t + f) * SW + row % SW] = from_f32<T>(x);
         }
       }
@@ -760,7 +766,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     lk.put(sm + L::K);
     fence_proxy_async_smem();
     tc_fence_before_sync();
-    const bool redo = __syncthreads_or(bad != 0.f);  // a sum of zeros unless a value is not finite
+    // a sum of zeros unless a value is not finite (one of the rows past the chunk's tokens, then,
+    // costs time and nothing else)
+    const bool redo = __syncthreads_or(bad != 0.f && row < a.dv);
     tc_fence_after_sync();
     // the next chunk's scores may take O1's place: its q and k have come meanwhile
     if (more) issue_scores(ph ^ 1);
