@@ -32,60 +32,79 @@ struct Unit {
   int slot0;  // workspace state of the sequence's unit 0 (sequences of several units)
   bool found;
 };
-// Unit u of the call, in sequence order: a whole CTA adds up the units of the sequences
-// before it. `n_ws`: states in the workspace; a sequence whose units would not fit (offsets
-// that descend can make sequences share tokens) is not found. `scratch`: 4 + 2 * (threads / 32)
-// ints of shared memory.
+constexpr int UNIT_SCRATCH = 4 + 3 * 8;  // ints of shared memory that find_unit takes (8 warps)
+// Unit u of the call: u < B are the last (or only) units of the sequences, u >= B counts the
+// others, each of seg tokens, in sequence order. Of up to 256 sequences the last units of more
+// than half of seg come first, so that a grid in this order ends with its shortest pieces. A
+// whole CTA of 256 threads adds up what the sequences before it have. `n_ws`: states in the
+// workspace; a sequence whose units would not fit (offsets that descend can make sequences
+// share tokens) is not found.
 __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_ws, int u, int* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool ranked = a.B <= 256;
+  Unit r{0, 0, 1, 0, true};
+  if (u < a.B && (a.B == 1 || !ranked)) {
+    int begin, end;
+    seq_range(a, u, begin, end);
+    r.b = u;
+    r.n = seq_units(end - begin, seg);
+    r.i = r.n - 1;
+    if (r.n == 1) return r;
+  }
   int base_u = 0, base_s = 0;
   if (tid == 0) scratch[0] = -1;
-  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+  for (int b0 = 0; b0 < a.B; b0 += 256) {
     const int b = b0 + tid;
-    int nu = 0;
+    int ns = 0, tail = 0;
     if (b < a.B) {
       int begin, end;
       seq_range(a, b, begin, end);
-      nu = seq_units(end - begin, seg);
+      ns = seq_units(end - begin, seg);
+      tail = end - begin - (ns - 1) * seg;
     }
-    const int ns = nu > 1 ? nu : 0;
-    int cu = nu, cs = ns;  // inclusive sums over the warp
+    const int nu = max(ns - 1, 0);                // units but the last
+    const int nl = tail > seg / 2;                // whether the last one is long
+    if (ns == 1) ns = 0;                          // states
+    int cu = nu, cs = ns, cl = nl;                // inclusive sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, cu, o), y = __shfl_up_sync(0xffffffffu, cs, o);
+      const int z = __shfl_up_sync(0xffffffffu, cl, o);
       if (lane >= o) {
         cu += x;
         cs += y;
+        cl += z;
       }
     }
     __syncthreads();  // the last round's sums have been read
     if (lane == 31) {
-      scratch[4 + 2 * warp] = cu;
-      scratch[5 + 2 * warp] = cs;
+      scratch[4 + 3 * warp] = cu;
+      scratch[5 + 3 * warp] = cs;
+      scratch[6 + 3 * warp] = cl;
     }
     __syncthreads();
-    int pu = base_u, ps = base_s;
-    for (int w = 0; w < nw; ++w) {
-      const int x = scratch[4 + 2 * w], y = scratch[5 + 2 * w];
+    int pu = base_u + cu - nu, ps = base_s + cs - ns, pl = cl - nl, longs = 0;
+    for (int w = 0; w < 8; ++w) {
+      const int x = scratch[4 + 3 * w], y = scratch[5 + 3 * w], z = scratch[6 + 3 * w];
       if (w < warp) {
         pu += x;
         ps += y;
+        pl += z;
       }
       base_u += x;
       base_s += y;
+      longs += z;
     }
-    pu += cu - nu;
-    ps += cs - ns;
-    if (u >= pu && u < pu + nu) {
+    const int rank = !ranked ? b : nl ? pl : longs + b - pl;
+    if (b < a.B && (u < a.B ? rank == u : u - a.B >= pu && u - a.B < pu + nu)) {
       scratch[0] = b;
-      scratch[1] = u - pu;
-      scratch[2] = nu;
+      scratch[1] = u < a.B ? nu : u - a.B - pu;
+      scratch[2] = nu + 1;
       scratch[3] = ps;
     }
-    if (u < base_u) break;
+    if (u < a.B ? u < b0 + 256 : u - a.B < base_u) break;
   }
   __syncthreads();
-  Unit r;
   r.b = scratch[0];
   r.i = scratch[1];
   r.n = scratch[2];

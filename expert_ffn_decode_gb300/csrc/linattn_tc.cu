@@ -71,7 +71,7 @@ struct Misc {
   uint64_t full_q, full_k, full_v;  // a tile has landed
   uint64_t qk, qs, end;             // products are done
   uint32_t tmem;
-  int scratch[4 + 16];
+  int scratch[UNIT_SCRATCH];
   // f16: largest magnitudes on the way to the scales, and the scores' inverse scales
   alignas(16) float pinv[CH];
   float kmax[8], smax[2][128], pmax[2][32];
@@ -370,10 +370,15 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, quarter = warp & 3;
   const bool iwarp = __shfl_sync(0xffffffffu, warp, 0) == 3;  // whose elected lane issues
-  const int h = blockIdx.y, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
+  // The heads of a unit are neighbours. Whole units come first and the sequences' last ones,
+  // of any length, fill what is left (143 -> 120 us for a ragged batch of 9 prompts); the state
+  // pass has no last units.
+  const int h = blockIdx.x % a.H, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
+  const int whole = (int)(gridDim.x / a.H) - a.B, at = blockIdx.x / a.H;  // MODE 1: units but the last, at most
+  const int u = MODE == 0 || at < whole ? a.B + at : at - whole;
   pdl_wait_prior_grids();
-  const Unit un = find_unit(a, seg, n_ws, blockIdx.x, m->scratch);
-  if (!un.found || (MODE == 0 && un.i == un.n - 1)) return;
+  const Unit un = find_unit(a, seg, n_ws, u, m->scratch);
+  if (!un.found) return;
   int begin, end;
   seq_range(a, un.b, begin, end);
   const int last = end;
@@ -821,12 +826,13 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 }
 
 // The states before the units of each sequence of several: unit 0's is the sequence's own, and
-// each next one adds what the unit between leaves, in order.
+// each next one adds what the unit between leaves, in order. A thread keeps eight units of
+// four values in flight.
 __global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws, const float* wd, float* wst) {
-  __shared__ int scratch[4 + 16];
+  __shared__ int scratch[UNIT_SCRATCH];
   pdl_wait_prior_grids();
-  const Unit un = find_unit(a, seg, n_ws, blockIdx.x, scratch);
-  if (!un.found || un.i != 0 || un.n == 1) return;
+  const Unit un = find_unit(a, seg, n_ws, a.B + blockIdx.x, scratch);
+  if (!un.found || un.i != 0) return;
   const int slot = seq_slot(a, un.b);
   if (slot < 0) return;
   const int64_t sz = (int64_t)a.dk * a.dv, step = a.H * sz;
@@ -836,12 +842,23 @@ __global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws
   float4 s = a.fresh ? make_float4(0.f, 0.f, 0.f, 0.f)
                      : *reinterpret_cast<const float4*>(a.state + ((int64_t)slot * a.H + h) * sz + i);
   *reinterpret_cast<float4*>(w) = s;
-  for (int u = 1; u < un.n; ++u) {
-    w += step;
-    const float lam = wd[(int64_t)(un.slot0 + u - 1) * a.H + h];
-    const float4 x = *reinterpret_cast<const float4*>(w);
-    s = make_float4(fmaf(lam, s.x, x.x), fmaf(lam, s.y, x.y), fmaf(lam, s.z, x.z), fmaf(lam, s.w, x.w));
-    *reinterpret_cast<float4*>(w) = s;
+  constexpr int AHEAD = 8;  // units in flight
+  for (int u0 = 1; u0 < un.n; u0 += AHEAD) {
+    float4 x[AHEAD];
+    float lam[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (u0 + j < un.n) {
+        x[j] = *reinterpret_cast<const float4*>(w + (u0 + j) * step);
+        lam[j] = wd[(int64_t)(un.slot0 + u0 + j - 1) * a.H + h];
+      }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (u0 + j < un.n) {
+        s = make_float4(fmaf(lam[j], s.x, x[j].x), fmaf(lam[j], s.y, x[j].y), fmaf(lam[j], s.z, x[j].z),
+                        fmaf(lam[j], s.w, x[j].w));
+        *reinterpret_cast<float4*>(w + (u0 + j) * step) = s;
+      }
   }
 }
 
@@ -899,17 +916,18 @@ cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream
     if ((e = make_map(&maps.v, a.v, a.dv, a.H, a.N, a.vs, true)) != cudaSuccess) return e;
     if ((e = make_map(&maps.o, a.o, a.dv, a.H, a.N, a.os, false)) != cudaSuccess) return e;
   }
-  const dim3 grid((unsigned)sp.units, (unsigned)a.H);
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
-  const bool several = a.offsets ? sp.units > a.B : a.seq_len > sp.seg;
-  if (several) {
-    e = launch(lin_chunk<T, NP, 0, WIDE>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
+  const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.seg * a.B;  // units but the last, at most
+  if (whole > 0) {
+    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst,
+               ctrl);
     if (e != cudaSuccess) return e;
-    const dim3 jgrid((unsigned)sp.units, (unsigned)a.H, (unsigned)((a.dk * a.dv + 1023) / 1024));
+    const dim3 jgrid((unsigned)whole, (unsigned)a.H, (unsigned)((a.dk * a.dv + 1023) / 1024));
     e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1, WIDE>, grid, smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst, ctrl);
+  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
+                wd, wst, ctrl);
 }
 
 }  // namespace
