@@ -31,8 +31,6 @@
 namespace moe {
 namespace {
 
-constexpr int MV_WARPS = 8;
-constexpr int MV_DEPTH = 4;      // stages of a warp's ring: three in flight
 constexpr int MV_PITCH = 176;    // bytes of a staged row: 256 values of the widest type and 16 of misalignment;
                                  // 48 mod 128 spreads four 20-byte blocks of 8 rows over all banks
 constexpr int MV_SPITCH = 32;    // planes: staged bytes of a row's scales (and of its offsets)
@@ -49,6 +47,9 @@ struct Cols {
   static constexpr int NT = NT_, PARTS = PARTS_;
   static constexpr int VECS = MULTI ? 8 * NT / PARTS : 1;
   static constexpr int XBYTES = MULTI ? 16 * NT : 4;  // bytes of x pieces for each of a row's values
+  // Warps of a CTA and stages of a warp's ring (all but one in flight). Several vectors' x pieces
+  // leave room for one CTA an SM, which then has sixteen warps to share them.
+  static constexpr int WARPS = MULTI ? 16 : 8, DEPTH = MULTI ? 2 : 4;
 };
 
 struct MvArgs {
@@ -103,29 +104,20 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // values of a vector; the eight threads of a block are neighbours. Values past the row's end
 // are not written: they belong to blocks whose sums are dropped.
 template <int RT, class C>
-__device__ __forceinline__ void put_x(float4 v, int vec, int at, uint8_t* xf, float2* info) {
-  float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-  float sum = (v.x + v.y) + (v.z + v.w);
-  const unsigned group = 0xffu << (threadIdx.x & 24);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(group, mx, o));
-    sum += __shfl_xor_sync(group, sum, o);
-  }
+__device__ __forceinline__ void put_x(float4 v, float mx, float sum, int vec, int at, uint8_t* xf, float2* info) {
   // largest magnitude 2^e (1 .. 2): scale 2^(13 - e); it and 2^10 / it stay normal
   const int e = min(max((int)(__float_as_uint(mx) >> 23), 27), 253);
   const float sc = __uint_as_float((uint32_t)(267 - e) << 23);
   const float back = __uint_as_float((uint32_t)(e - 13) << 23);  // 1 / sc
   const int b = at / 32, r = at % 32;
   const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
-  float hi[4], lo[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    hi[j] = __half2float(__float2half_rn(f[j]));
-    lo[j] = f[j] - hi[j];
+  uint2 parts[2];
+  parts[0] = make_uint2(pack_h2(f[0], f[2]), pack_h2(f[1], f[3]));
+  if (C::PARTS == 2) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&parts[0].x));
+    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&parts[0].y));
+    parts[1] = make_uint2(pack_h2(f[0] - a.x, f[2] - a.y), pack_h2(f[1] - c.x, f[3] - c.y));
   }
-  const uint2 parts[2] = {make_uint2(pack_h2(hi[0], hi[2]), pack_h2(hi[1], hi[3])),
-                          make_uint2(pack_h2(lo[0], lo[2]), pack_h2(lo[1], lo[3]))};
   if constexpr (!C::MULTI) {
     int quad = b / 4, t = b & 3, nib = r / 16;
     if (RT == ROW_Q4_K) {  // lane t: 16 bytes, half t % 2 of a run of 64; nibble: which sub-block of it
@@ -151,20 +143,50 @@ __device__ __forceinline__ void put_x(float4 v, int vec, int at, uint8_t* xf, fl
 template <int RT, class C, typename TX>
 __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t* xf, float2* info) {
   const TX* x = static_cast<const TX*>(p.a.x) + t0 * p.a.xs;
-  constexpr int AHEAD = 4, NTH = MV_WARPS * 32;  // loads in flight of a thread
-  const int per = p.a.cols / 4, total = per * nv;  // a multiple of 8: a block's 8 threads stay together
-  for (int i0 = threadIdx.x; i0 < total; i0 += NTH * AHEAD) {
-    float4 ld[AHEAD];
+  constexpr int AHEAD = 4, STEP = C::WARPS * 32 * 4;  // pieces of a turn; values between a thread's pieces
+  const int cols = p.a.cols;
+  // The thread's pieces run through the vectors end to end; the next turn's are loaded before
+  // this one's are converted.
+  int vec = 0, at = threadIdx.x * 4;
+  while (at >= cols) at -= cols, ++vec;
+  int lv[AHEAD], la[AHEAD];
+  float4 ld[AHEAD];
+  auto fetch = [&]() {
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
-      const int i = min(i0 + n * NTH, total - 1);
-      ld[n] = load4(x + i / per * p.a.xs + i % per * 4);
+      lv[n] = vec;
+      la[n] = at;
+      ld[n] = vec < nv ? load4(x + vec * p.a.xs + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+      at += STEP;
+      while (at >= cols) at -= cols, ++vec;
     }
+  };
+  fetch();
+  const int turns = (cols * nv + STEP * AHEAD - 1) / (STEP * AHEAD);
+  for (int turn = 0; turn < turns; ++turn) {
+    float4 v[AHEAD];
+    int vv[AHEAD], va[AHEAD];
+    float mx[AHEAD], sum[AHEAD];
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
-      const int i = i0 + n * NTH;
-      if (i < total) put_x<RT, C>(ld[n], i / per, i % per * 4, xf, info);
+      v[n] = ld[n];
+      vv[n] = lv[n];
+      va[n] = la[n];
+      mx[n] = fmaxf(fmaxf(fabsf(v[n].x), fabsf(v[n].y)), fmaxf(fabsf(v[n].z), fabsf(v[n].w)));
+      sum[n] = (v[n].x + v[n].y) + (v[n].z + v[n].w);
     }
+    if (turn + 1 < turns) fetch();
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {  // over the 8 threads of a block
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) {
+        mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], o));
+        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], o);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n)
+      if (vv[n] < nv) put_x<RT, C>(v[n], mx[n], sum[n], vv[n], va[n], xf, info);
   }
 }
 
@@ -191,16 +213,17 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int byt
 // A warp's steps: the tiles of its group in turn, and in each its range of runs. Each step's rows are copied to the warp's own ring, three steps ahead, so a
 // warp never waits for another one but to join the partial sums of a tile.
 template <int RT, class C>
-__global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_constant__ MvArgs p) {
+__global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel(const __grid_constant__ MvArgs p) {
   extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int WARPS = C::WARPS, DEPTH = C::DEPTH;
   constexpr int STAGE = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = sm + warp * MV_DEPTH * STAGE;
-  uint8_t* xf = sm + MV_WARPS * MV_DEPTH * STAGE;
+  uint8_t* ring = sm + warp * DEPTH * STAGE;
+  uint8_t* xf = sm + WARPS * DEPTH * STAGE;
   float2* info = reinterpret_cast<float2*>(xf + (size_t)(p.nu * 256) * C::XBYTES);
   float* red = reinterpret_cast<float*>(info + p.nu * 8 * C::VECS);  // [2][warps][16 * VECS]
-  float4* zero = reinterpret_cast<float4*>(red + 2 * MV_WARPS * 16 * C::VECS);
-  const int groups = MV_WARPS / p.ks, group = warp / p.ks, part = warp % p.ks;
+  float4* zero = reinterpret_cast<float4*>(red + 2 * WARPS * 16 * C::VECS);
+  const int groups = WARPS / p.ks, group = warp / p.ks, part = warp % p.ks;
   const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
   const int ua = p.nu * part / p.ks, ub = p.nu * (part + 1) / p.ks, per_tile = ub - ua;
   const int my_tiles = first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
@@ -227,7 +250,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
   uint32_t c_at = smem_addr(ring);               // its stage
   const uint8_t* c_src = p.a.w + (int64_t)first * 16 * p.row_bytes + ua * RUN;
   const int64_t next_tile = (int64_t)stride * 16 * p.row_bytes - (int64_t)(per_tile - 1) * RUN;
-  const uint32_t ring_end = c_at + (MV_DEPTH - 1) * STAGE;
+  const uint32_t ring_end = c_at + (DEPTH - 1) * STAGE;
   auto copy_step = [&]() {
     if (c_left > 0) {
       if (c_tile + 1 < p.tiles && c_u * 8 + 8 <= p.nb) {
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
         }
       }
       --c_left;
-      c_at = c_at == ring_end ? ring_end - (MV_DEPTH - 1) * STAGE : c_at + STAGE;
+      c_at = c_at == ring_end ? ring_end - (DEPTH - 1) * STAGE : c_at + STAGE;
       if (++c_u == ub) {
         c_u = ua;
         c_tile += stride;
@@ -265,7 +288,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < MV_DEPTH - 1; ++i) copy_step();
+  for (int i = 0; i < DEPTH - 1; ++i) copy_step();
 
   // ---- x ------------------------------------------------------------------------------
   pdl_wait_prior_grids();
@@ -313,7 +336,18 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
   uint4 x[2][4];  // single vector: the pieces of a run, kept from tile to tile if there is one run
   float2 xin[2];
   int stage = 0;
+  const bool add = (p.a.flags & MOE_ACCUMULATE) != 0;
   for (int k = 0, tile = first; k < my_tiles; ++k, tile += stride) {
+    // what a single vector's sums will be added to, loaded while they are made
+    float old = 0.f;
+    if (!C::MULTI && part * 32 + lane < 16 && tile * 16 + lane < p.a.rows) {
+      const int64_t row = (int64_t)tile * 16 + lane, at = t0 * p.a.ys + row;
+      if (add)
+        old = p.a.y_type == MOE_F32   ? static_cast<const float*>(p.a.y)[at]
+              : p.a.y_type == MOE_F16 ? __half2float(static_cast<const __half*>(p.a.y)[at])
+                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.a.y)[at]);
+      if (p.a.bias) old += p.a.bias[row];
+    }
     for (int u0 = ua; u0 < ub; ++u0) {
       if constexpr (!C::MULTI) {
         if (k == 0 || per_tile > 1) {
@@ -328,10 +362,10 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
                 xl[i / 2 % 2] + (xstep[i / 2 % 2] ? (u0 * 2 + i / 4) * 512 + (i & 1) * 128 : 0));
         }
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(MV_DEPTH - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
       __syncwarp();
       const uint8_t* st = ring + stage;
-      stage = stage == (MV_DEPTH - 1) * STAGE ? 0 : stage + STAGE;
+      stage = stage == (DEPTH - 1) * STAGE ? 0 : stage + STAGE;
       const uint8_t* base[2];
       const uint8_t* sbase[2];
 #pragma unroll
@@ -466,7 +500,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
       copy_step();
     }
     // ---- join the partial sums of the tile, in order ------------------------------------
-    float* mine = red + ((k & 1) * MV_WARPS + warp) * 16 * C::VECS;
+    float* mine = red + ((k & 1) * WARPS + warp) * 16 * C::VECS;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -487,21 +521,20 @@ __global__ void __launch_bounds__(MV_WARPS * 32, 2) matvec_kernel(const __grid_c
     for (int i = part * 32 + lane; i < 16 * nv; i += p.ks * 32) {
       const int64_t row = (int64_t)tile * 16 + i % 16;
       if (row >= p.a.rows) continue;
-      const float* from = red + ((k & 1) * MV_WARPS + group * p.ks) * 16 * C::VECS + i;
+      const float* from = red + ((k & 1) * WARPS + group * p.ks) * 16 * C::VECS + i;
       float s = 0.f;
       for (int w = 0; w < p.ks; ++w) s += from[w * 16 * C::VECS];
-      if (p.a.bias) s += p.a.bias[row];
       const int64_t at = (t0 + i / 16) * p.a.ys + row;
-      const bool add = (p.a.flags & MOE_ACCUMULATE) != 0;
+      if (C::MULTI && p.a.bias) s += p.a.bias[row];
       if (p.a.y_type == MOE_F32) {
         float* y = static_cast<float*>(p.a.y) + at;
-        *y = add ? *y + s : s;
+        *y = s + (!C::MULTI ? old : add ? *y : 0.f);
       } else if (p.a.y_type == MOE_F16) {
         __half* y = static_cast<__half*>(p.a.y) + at;
-        *y = __float2half_rn(add ? __half2float(*y) + s : s);
+        *y = __float2half_rn(s + (!C::MULTI ? old : add ? __half2float(*y) : 0.f));
       } else {
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.a.y) + at;
-        *y = __float2bfloat16_rn(add ? __bfloat162float(*y) + s : s);
+        *y = __float2bfloat16_rn(s + (!C::MULTI ? old : add ? __bfloat162float(*y) : 0.f));
       }
     }
   }
@@ -514,8 +547,8 @@ constexpr int MV_SMEM = 227 * 1024;     // shared memory of a CTA at most
 template <int RT, class C>
 int smem_bytes(const MvArgs& p) {
   const int stage = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
-  return MV_WARPS * MV_DEPTH * stage + p.nu * 256 * C::XBYTES + p.nu * 8 * C::VECS * 8 +
-         2 * MV_WARPS * 16 * C::VECS * 4 + 16;
+  return C::WARPS * C::DEPTH * stage + p.nu * 256 * C::XBYTES + p.nu * 8 * C::VECS * 8 +
+         2 * C::WARPS * 16 * C::VECS * 4 + 16;
 }
 
 template <int RT, class C>
@@ -523,12 +556,12 @@ cudaError_t launch(MvArgs& p, cudaStream_t st) {
   const int smem = smem_bytes<RT, C>(p);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(matvec_kernel<RT, C>), smem);
   if (e != cudaSuccess) return e;
-  const int ctas = smem <= 113 * 1024 ? MV_CTAS : MV_CTAS / 2;
+  const int ctas = !C::MULTI && smem <= 113 * 1024 ? MV_CTAS : MV_CTAS / 2;
   // Warps that share a tile: the count whose slowest warp has the fewest runs to walk, and the
   // larger one when two tie (fewer rows wait for a warp).
   int64_t best = -1;
-  for (int ks = MV_WARPS; ks >= 1; ks /= 2) {
-    const int per = MV_WARPS / ks;
+  for (int ks = C::WARPS; ks >= C::WARPS / 8; ks /= 2) {  // (at most 8 groups have a barrier of their own)
+    const int per = C::WARPS / ks;
     const int64_t rounds = (p.tiles + (int64_t)ctas * per - 1) / ((int64_t)ctas * per);
     const int64_t cost = rounds * ((p.nu + ks - 1) / ks * 8 + (ks > 1 ? 1 : 0));
     if (best < 0 || cost < best) {
@@ -536,11 +569,11 @@ cudaError_t launch(MvArgs& p, cudaStream_t st) {
       p.ks = ks;
     }
   }
-  const int per = MV_WARPS / p.ks;
+  const int per = C::WARPS / p.ks;
   const int want = (p.tiles + per - 1) / per;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(want < ctas ? want : ctas), (unsigned)((p.a.T + C::VECS - 1) / C::VECS));
-  cfg.blockDim = dim3(MV_WARPS * 32);
+  cfg.blockDim = dim3(C::WARPS * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
