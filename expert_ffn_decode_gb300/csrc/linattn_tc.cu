@@ -827,38 +827,52 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 
 // The states before the units of each sequence of several: unit 0's is the sequence's own, and
 // each next one adds what the unit between leaves, in order. A thread keeps eight units of
-// four values in flight.
-__global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws, const float* wd, float* wst) {
+// 2 x 4 values in flight. `by_seq`: a CTA for each sequence, else for each unit, of which the
+// first does the work (many sequences, few of them long).
+__global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws, int by_seq, const float* wd,
+                                                float* wst) {
   __shared__ int scratch[UNIT_SCRATCH];
   pdl_wait_prior_grids();
-  const Unit un = find_unit(a, seg, n_ws, a.B + blockIdx.x, scratch);
-  if (!un.found || un.i != 0) return;
+  const Unit un = find_unit(a, seg, n_ws, by_seq ? blockIdx.x : a.B + blockIdx.x, scratch);
+  if (!un.found || un.n == 1 || (!by_seq && un.i != 0)) return;
   const int slot = seq_slot(a, un.b);
   if (slot < 0) return;
   const int64_t sz = (int64_t)a.dk * a.dv, step = a.H * sz;
-  const int i = (blockIdx.z * 256 + threadIdx.x) * 4, h = blockIdx.y;
-  if (i >= sz) return;
-  float* w = wst + ((int64_t)un.slot0 * a.H + h) * sz + i;
-  float4 s = a.fresh ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : *reinterpret_cast<const float4*>(a.state + ((int64_t)slot * a.H + h) * sz + i);
-  *reinterpret_cast<float4*>(w) = s;
-  constexpr int AHEAD = 8;  // units in flight
+  const int h = blockIdx.y, at = (blockIdx.z * 512 + threadIdx.x) * 4;
+  const float* pool = a.state + ((int64_t)slot * a.H + h) * sz;
+  float* w = wst + ((int64_t)un.slot0 * a.H + h) * sz;
+  float4 s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = at + k * 1024;
+    if (i >= sz) continue;
+    s[k] = a.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(pool + i);
+    *reinterpret_cast<float4*>(w + i) = s[k];
+  }
+  constexpr int AHEAD = 8;
   for (int u0 = 1; u0 < un.n; u0 += AHEAD) {
-    float4 x[AHEAD];
+    float4 x[AHEAD][2];
     float lam[AHEAD];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (u0 + j < un.n) {
-        x[j] = *reinterpret_cast<const float4*>(w + (u0 + j) * step);
-        lam[j] = wd[(int64_t)(un.slot0 + u0 + j - 1) * a.H + h];
-      }
+    for (int j = 0; j < AHEAD; ++j) {
+      const int u = min(u0 + j, un.n - 1);
+      lam[j] = wd[(int64_t)(un.slot0 + u - 1) * a.H + h];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (u0 + j < un.n) {
-        s = make_float4(fmaf(lam[j], s.x, x[j].x), fmaf(lam[j], s.y, x[j].y), fmaf(lam[j], s.z, x[j].z),
-                        fmaf(lam[j], s.w, x[j].w));
-        *reinterpret_cast<float4*>(w + (u0 + j) * step) = s;
+      for (int k = 0; k < 2; ++k)
+        if (at + k * 1024 < sz) x[j][k] = *reinterpret_cast<const float4*>(w + u * step + at + k * 1024);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (u0 + j >= un.n) break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = at + k * 1024;
+        if (i >= sz) continue;
+        s[k] = make_float4(fmaf(lam[j], s[k].x, x[j][k].x), fmaf(lam[j], s[k].y, x[j][k].y),
+                           fmaf(lam[j], s[k].z, x[j][k].z), fmaf(lam[j], s[k].w, x[j][k].w));
+        *reinterpret_cast<float4*>(w + (u0 + j) * step + i) = s[k];
       }
+    }
   }
 }
 
@@ -922,8 +936,9 @@ cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream
     e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst,
                ctrl);
     if (e != cudaSuccess) return e;
-    const dim3 jgrid((unsigned)whole, (unsigned)a.H, (unsigned)((a.dk * a.dv + 1023) / 1024));
-    e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, (const float*)wd, wst);
+    const int by_seq = a.B <= whole;
+    const dim3 jgrid((unsigned)(by_seq ? a.B : whole), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
+    e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, by_seq, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
   return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
