@@ -193,10 +193,12 @@ def lib():
 def _ptr(obj):
     if obj is None:
         return None
+    try:  # the common case first: this is a good part of a small call's host time
+        return obj.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(obj, int):
         return obj
-    if hasattr(obj, "data_ptr"):
-        return obj.data_ptr()
     if hasattr(obj, "ctypes"):
         return obj.ctypes.data
     raise TypeError(f"cannot pass {type(obj).__name__} as a pointer")
