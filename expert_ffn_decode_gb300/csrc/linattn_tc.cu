@@ -916,8 +916,8 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int t
 }
 
 template <typename T, int NP, bool WIDE>
-cudaError_t chunk_launch(const LinattnArgs& a, uint8_t* ws, bool pdl, cudaStream_t st) {
-  const LinattnSplit sp = linattn_split(a.N, a.B, a.H, a.dk, a.dv);
+cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, cudaStream_t st) {
+  const LinattnSplit sp = linattn_split(a.N, a.B, a.H, a.dk, a.dv, type);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws);
   float* wd = reinterpret_cast<float*>(ws + sp.decays);
   float* wst = reinterpret_cast<float*>(ws + sp.states);
@@ -951,11 +951,11 @@ cudaError_t linattn_chunk_launch(const LinattnArgs& a, int type, void* ws, bool 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool wide = a.dk > 112;
   if (type == MOE_F32)
-    return wide ? chunk_launch<float, 3, true>(a, w, pdl, st) : chunk_launch<float, 3, false>(a, w, pdl, st);
+    return wide ? chunk_launch<float, 3, true>(a, type, w, pdl, st) : chunk_launch<float, 3, false>(a, type, w, pdl, st);
   if (type == MOE_F16)
-    return wide ? chunk_launch<__half, 1, true>(a, w, pdl, st) : chunk_launch<__half, 1, false>(a, w, pdl, st);
-  return wide ? chunk_launch<__nv_bfloat16, 1, true>(a, w, pdl, st)
-              : chunk_launch<__nv_bfloat16, 1, false>(a, w, pdl, st);
+    return wide ? chunk_launch<__half, 1, true>(a, type, w, pdl, st) : chunk_launch<__half, 1, false>(a, type, w, pdl, st);
+  return wide ? chunk_launch<__nv_bfloat16, 1, true>(a, type, w, pdl, st)
+              : chunk_launch<__nv_bfloat16, 1, false>(a, type, w, pdl, st);
 }
 
 }  // namespace moe

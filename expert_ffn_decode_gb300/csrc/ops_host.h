@@ -46,21 +46,26 @@ struct LinattnArgs {
   int fresh, token_decay;
 };
 // How a prompt call is cut: sequences into units of `seg` tokens (a multiple of 64), so that
-// units x heads fill the GPU's 304 CTA places about once (152 SMs, two CTAs each); at least
-// LINATTN_MIN_SEG tokens, since a cut costs a second pass over k and v and a state's round
-// trip. `units` bounds their number from what the host knows, `n_ws` the states that
-// sequences of several units keep in the workspace; the rest are byte offsets in it.
-constexpr int LINATTN_MIN_SEG = 256;
+// units x heads fill the GPU's CTA places about once (152 SMs, two CTAs each; one for f32). A cut
+// costs a second pass over k and v, a state's round trip and two launches: one sequence with
+// 16 heads of 128 in bf16 takes 21 us whole and 24 cut at 320 tokens, 30 and 25 at 512, 56 and
+// 27 at 1024; units of 128 tokens against 256 take 25 and 35 us at 512, 52 and 50 at 4096.
+// `units` bounds their number from what the host knows, `n_ws` the states that sequences of
+// several units keep in the workspace; the rest are byte offsets in it.
+constexpr int LINATTN_MIN_SEG = 128;
 struct LinattnSplit {
   int seg, units, n_ws;
   size_t decays, states, total;
 };
-inline LinattnSplit linattn_split(int N, int B, int H, int dk, int dv) {
+inline LinattnSplit linattn_split(int N, int B, int H, int dk, int dv, int type) {
   LinattnSplit s{};
-  const int want = 304 / H > 1 ? 304 / H : 1;
+  const int places = type == MOE_F32 ? 152 : 304;
+  const int want = places / H > 1 ? places / H : 1;
   int64_t seg = ((int64_t)N + want - 1) / want;
   seg = (seg + 63) / 64 * 64;
   if (seg < LINATTN_MIN_SEG) seg = LINATTN_MIN_SEG;
+  const int whole = type == MOE_F32 ? 256 : 384;  // f32: 47 us whole and 47 cut at 256 tokens, 57 and 46 at 320
+  if (N <= whole) seg = whole;
   s.seg = seg > 1 << 30 ? 1 << 30 : (int)seg;
   s.units = N / s.seg + B;       // sum of ceil(n_b / seg), an empty sequence counting one
   s.n_ws = 2 * (N / s.seg);      // a sequence longer than seg has at most 2 n_b / seg units
