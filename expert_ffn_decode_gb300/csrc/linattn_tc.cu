@@ -14,12 +14,12 @@
 // shared memory, and a thread owns half a row of S^T in f32 registers.
 //
 // Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; an
-// f32 one splits into three bf16 parts (8 bits each, 24 in all). Scores and the state as an
-// operand keep two parts for 16-bit types (16 bits in bf16, 22 in f16) and three for f32. The
-// decayed keys are summed into the f32 state, so they keep f32's bits whatever the type:
-// three bf16 parts or two f16 ones. f16 parts need their values in f16's range: scores and
-// states are scaled by a power of two for each row, decayed keys for each chunk. Products of
-// parts below the last kept bit are left out. Sums, statistics and the state are f32.
+// f32 one becomes two f16 parts (22 bits) of its value times a power of two for the chunk's
+// tile. Scores and the state as an operand keep two parts (16 bits in bf16, 22 in f16). The
+// decayed keys are summed into the f32 state, so they keep more bits for bf16 too: three
+// bf16 parts (24) or two f16 ones. f16 parts need their values in f16's range: scores and
+// states are scaled by a power of two for each row, decayed keys for each chunk. The product
+// of two low parts is left out. Sums, statistics and the state are f32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -42,16 +42,14 @@ __host__ __device__ constexpr uint32_t p_pitch(int i) { return 16u * (64 - 16 * 
 
 template <int NP>
 struct Plan {
-  static constexpr int NPP = NP == 3 ? 3 : 2;  // parts of scores and state operands
+  static constexpr int NPP = 2;  // parts of scores and state operands
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
-  static constexpr uint32_t P = KT + 3 * TILE;
+  static constexpr uint32_t P = KT + (NP == 1 ? 3 : 2) * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
   static constexpr uint32_t BYTES = MISC + 5760;  // NP 1: 114,304 bytes and 1,024 of slack, two CTAs an SM
   // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
-  // their place once O2 is done where there are two of them (a thread's columns of A are its
-  // columns of the parts).
-  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = NP == 3 ? 320 : 128;
-  static constexpr uint32_t T_COLS = NP == 3 ? 512 : 256;
+  // their place once O2 is done (a thread's columns of A are its columns of the parts).
+  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128, T_COLS = 256;
 };
 
 struct Decays {
@@ -74,7 +72,7 @@ struct Misc {
   int scratch[UNIT_SCRATCH];
   // f16: largest magnitudes on the way to the scales, and the scores' inverse scales
   alignas(16) float pinv[CH];
-  float kmax[8], smax[2][128], pmax[2][32];
+  float kmax[8], smax[2][128], pmax[2][32], tmax[3][8];  // tmax: f32 q, k, v by warp
 };
 static_assert(sizeof(Misc) <= 5760, "misc");
 
@@ -186,47 +184,59 @@ __device__ __forceinline__ float2 f16_scale(float mx) {
 // along K, 128 along rows) and as an MN-major one (rows along K: 128 along K, 1024 along columns).
 __device__ __forceinline__ uint32_t piece(int kc, int row) { return (uint32_t)(kc * CH + row) * 16u; }
 
-// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] matrix that
-// needs several parts: four 8-column pieces of one row, fetched early and put into the tile
-// when that is free. A warp's 32 pieces of one i fill four whole 128-byte lines.
-template <typename T, int NP>
+// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] f32 matrix: four
+// 8-column pieces of one row, fetched early and put into the tile as two f16 parts when that
+// is free. A warp's 32 pieces of one i fill four whole 128-byte lines.
+template <int NP>
 struct Loader {
-  static constexpr int W = NP == 1 ? 4 : sizeof(T) * 2;  // 32-bit words of a piece
-  uint32_t r[NP == 1 ? 1 : D / 32][W];
-  __device__ __forceinline__ void fetch(const T* src, int64_t stride, int t0, int n, int dim) {
-    if constexpr (NP > 1) {
-      const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+  float r[NP == 1 ? 1 : D / 32][8];
+  __device__ __forceinline__ void fetch(const float* src, int64_t stride, int t0, int n, int dim) {
+    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int kc = i * 4 + (lane >> 3);
-        const bool in = row < n && kc * 8 < dim;
-        const T* p = in ? src + (t0 + row) * stride + kc * 8 : src;
+    for (int i = 0; i < D / 32; ++i) {
+      const int kc = i * 4 + (lane >> 3);
+      const bool in = row < n && kc * 8 < dim;
+      const float* p = in ? src + (t0 + row) * stride + kc * 8 : src;
 #pragma unroll
-        for (int j = 0; j < W / 4; ++j) {
-          const uint4 u = in ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
-          r[i][4 * j] = u.x;
-          r[i][4 * j + 1] = u.y;
-          r[i][4 * j + 2] = u.z;
-          r[i][4 * j + 3] = u.w;
-        }
+      for (int j = 0; j < 2; ++j) {
+        const float4 u = in ? reinterpret_cast<const float4*>(p)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        r[i][4 * j] = u.x;
+        r[i][4 * j + 1] = u.y;
+        r[i][4 * j + 2] = u.z;
+        r[i][4 * j + 3] = u.w;
       }
     }
   }
-  __device__ __forceinline__ void put(uint8_t* dst) const {
-    if constexpr (NP > 1) {
-      const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+  // Largest finite magnitude of the warp's pieces: an infinity or a NaN stays one whatever the
+  // scale, and must not take the others' bits.
+  __device__ __forceinline__ float warp_max() const {
+    float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t u[4][NP];
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          split_pair<NP>(__uint_as_float(r[i][2 * j]), __uint_as_float(r[i][2 * j + 1]), u[j]);
-        }
-        uint8_t* d = dst + piece(i * 4 + (lane >> 3), row);
+      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(r[i][j]));
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    if (mx > 3.402823466e38f) {
+      mx = 0.f;
 #pragma unroll
-        for (int q = 0; q < NP; ++q)
-          *reinterpret_cast<uint4*>(d + q * TILE) = make_uint4(u[0][q], u[1][q], u[2][q], u[3][q]);
-      }
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = isfinite(r[i][j]) ? fmaxf(mx, fabsf(r[i][j])) : mx;
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    }
+    return mx;
+  }
+  __device__ __forceinline__ void put(uint8_t* dst, float scale) const {
+    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t u[4][NP];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_pair<NP, true>(r[i][2 * j] * scale, r[i][2 * j + 1] * scale, u[j]);
+      uint8_t* d = dst + piece(i * 4 + (lane >> 3), row);
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+        *reinterpret_cast<uint4*>(d + q * TILE) = make_uint4(u[0][q], u[1][q], u[2][q], u[3][q]);
     }
   }
 };
@@ -362,9 +372,10 @@ template <typename T, int NP, int MODE, bool WIDE>
 __global__ void __launch_bounds__(256, NP == 1 ? 2 : 1)
 lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
   using L = Plan<NP>;
-  constexpr bool F16 = std::is_same<T, __half>::value;
-  constexpr int NPP = L::NPP, LIM = NP == 3 ? 2 : 1;  // products of parts i, j with i + j <= LIM
-  constexpr int KP = F16 ? 2 : 3;                     // parts of the decayed keys
+  constexpr bool F16 = !std::is_same<T, __nv_bfloat16>::value;  // the type of the parts
+  constexpr bool F32 = std::is_same<T, float>::value;
+  constexpr int NPP = L::NPP, LIM = 1;  // products of parts i, j with i + j <= LIM
+  constexpr int KP = F16 ? 2 : 3;       // parts of the decayed keys
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
@@ -420,13 +431,44 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, begin, &m->full_q);
     tma_load_tile(sm + L::V, &maps.v, a.dv, h, begin, &m->full_v);
   }
-  Loader<T, NP> lq, lk, lv;
-  if (NP > 1 && begin < end) {
-    const int n = min(CH, end - begin);
-    if (MODE == 1) lq.fetch(q, a.qs, begin, n, a.dk);
-    lk.fetch(k, a.ks, begin, n, a.dk);
-    if (MODE == 1) lq.put(sm + L::Q);
-    lk.put(sm + L::K);
+  // f32: a chunk's q, k and v on their way, and the scales (and their inverses) of their tiles
+  Loader<NP> lq, lk, lv;
+  float2 qsc = make_float2(1.f, 1.f), ksc = qsc, vsc = qsc;
+  float kmx = 0.f;
+  auto fetch = [&](int t0) {
+    if constexpr (F32) {
+      const int n = min(CH, end - t0);
+      if (MODE == 1) lq.fetch(q, a.qs, t0, n, a.dk);
+      lk.fetch(k, a.ks, t0, n, a.dk);
+      lv.fetch(v, a.vs, t0, n, a.dv);
+    }
+  };
+  auto write_max = [&]() {
+    if constexpr (F32) {
+      const float x = MODE == 1 ? lq.warp_max() : 0.f, y = lk.warp_max(), z = lv.warp_max();
+      if (lane == 0) m->tmax[0][warp] = x, m->tmax[1][warp] = y, m->tmax[2][warp] = z;
+    }
+  };
+  auto put_qk = [&]() {  // after a barrier behind write_max
+    if constexpr (F32) {
+      float mx[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) mx[i] = fmaxf(mx[i], m->tmax[i][w]);
+      qsc = f16_scale(mx[0]);
+      ksc = f16_scale(mx[1]);
+      vsc = f16_scale(mx[2]);
+      kmx = mx[1];
+      if (MODE == 1) lq.put(sm + L::Q, qsc.x);
+      lk.put(sm + L::K, ksc.x);
+    }
+  };
+  if (F32 && begin < end) {
+    fetch(begin);
+    write_max();
+    __syncthreads();
+    put_qk();
   }
   if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
 
@@ -539,28 +581,35 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     const bool more = t0 + CH < end;
     // the state pass has no q: v alternates between the two places
     uint8_t* tv = sm + (NP == 1 && MODE == 0 && ph ? L::Q : L::V);
-    if (NP > 1) {
+    if constexpr (F32) {
       fence_proxy_async_smem();
       __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
-      lv.fetch(v, a.vs, t0, n, a.dv);
+      lv.put(tv, vsc.x);
     }
-    if (t0 == begin) issue_scores(ph);
+    if (F32 || t0 == begin) issue_scores(ph);
     // ---- the decayed keys ---------------------------------------------------------------
     if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
-    if (NP == 1 && !F16 && t0 == begin) __syncthreads();  // the first decays
+    if (!F16 && t0 == begin) __syncthreads();  // the first decays
     float2 kscale = make_float2(1.f, 1.f);
-    if constexpr (F16) {
-      uint32_t mx = 0;  // as packed f16 bits, of which the unsigned order is that of magnitudes
+    if constexpr (F32) {
+      kscale = f16_scale(kmx * d->wmax);
+    } else if constexpr (F16) {
+      // largest finite magnitude, as packed f16 bits, of which the unsigned order is that of magnitudes
+      auto largest = [&](auto keep) {
+        uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
-        if (r < n && kc < 2 * ks) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sm + L::K + tile_piece<NP>(kc, r));
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                     __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        for (int i = 0; i < D / 32; ++i) {
+          const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
+          if (r < n && kc < 2 * ks) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sm + L::K + tile_piece<NP>(kc, r));
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(keep(u.x & 0x7fff7fffu), keep(u.y & 0x7fff7fffu)),
+                                       __vmaxu2(keep(u.z & 0x7fff7fffu), keep(u.w & 0x7fff7fffu))));
+          }
         }
-      }
-      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+        return __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      };
+      uint32_t mx = largest([](uint32_t u) { return u; });
+      if (mx >= 0x7c00u) mx = largest([](uint32_t u) { return u & __vcmpltu2(u, 0x7c007c00u); });
       if (lane == 0) m->kmax[warp] = __half2float(__ushort_as_half((unsigned short)mx));
       __syncthreads();  // also: the first decays
       float km = 0.f;
@@ -572,7 +621,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     for (int i = 0; i < D / 32; ++i) {
       const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
       if (i * 4 >= 2 * ks) break;
-      const float w = d->w[r] * kscale.x;
+      const float w = d->w[r] * kscale.x * ksc.y;
       float x[8];
       read_piece<NP, F16>(sm + L::K + tile_piece<NP>(kc, r), x);
       if (n < CH && r >= n) {  // rows past the chunk's tokens are other sequences' or none
@@ -591,7 +640,6 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       for (int i = n * 16 + tid; i < CH * 16; i += 256)
         *reinterpret_cast<uint4*>(tv + tile_piece<1>(i & 15, i >> 4)) = make_uint4(0, 0, 0, 0);
     }
-    lv.put(tv);
     sum_lo += d->glo;
     {
       const float s = sum_hi + d->ghi, bb = s - sum_hi;
@@ -606,11 +654,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       break;
     }
     tc_fence_after_sync();
-    if (NP > 1 && more) {
-      const int n1 = min(CH, end - t0 - CH);
-      if (MODE == 1) lq.fetch(q, a.qs, t0 + CH, n1, a.dk);
-      lk.fetch(k, a.ks, t0 + CH, n1, a.dk);
-    }
+    if (more) fetch(t0 + CH);
     if (warp == 7 && more) chunk_decays(a, h, t0 + CH, min(CH, end - t0 - CH), &m->d[ph ^ 1]);
     // ---- the state's share, and what the chunk adds to the state -------------------------
     if (iwarp && elect_one()) {
@@ -643,7 +687,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       ok = mbar_wait(&m->qk, ph) && ok;
       tc_fence_after_sync();
       const float4 gt = d->g[row];
-      const float et = d->eg[row];
+      const float qk = qsc.y * ksc.y, et = d->eg[row];
       uint32_t sc[2][16];
       float mx = 0.f;
 #pragma unroll
@@ -654,7 +698,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
         tmem_ld_wait();
         // exp(G_t - G_s): where the chunk's decays are mild, as a product of two factors (16-bit
         // types; a score that overflows on the way ends in the token-by-token form)
-        if (NP < 3 && d->mild) {
+        if (!F32 && d->mild) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 f = *reinterpret_cast<const float4*>(&d->ieg[step * 16 + 4 * j]);
@@ -668,7 +712,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
           for (int j = 0; j < 16; ++j) {
             const float4 gs = d->g[step * 16 + j];
             const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
-            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * x * a.scale) : 0u;
+            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * qk * x * a.scale) : 0u;
           }
         }
         if (wg == quarter) {  // (rows 32 .. 63 see all of the first 32 columns)
@@ -731,9 +775,10 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     ok = mbar_wait(&m->end, ph) && ok;
     tc_fence_after_sync();
     if (MODE == 0) {
-      add_state(d->lam, kscale.y);
-      lk.put(sm + L::K);
-      if (NP == 1) __syncthreads();  // the next decays are there
+      add_state(d->lam, kscale.y * vsc.y);
+      if (F32 && more) write_max();
+      __syncthreads();  // the next decays are there
+      if (F32 && more) put_qk();
       continue;
     }
     // ---- outputs ----------------------------------------------------------------------
@@ -741,6 +786,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     // ones for 32-bit types, two halves of 64 channels otherwise.
     T* stage = reinterpret_cast<T*>(sm + L::V);
     constexpr int SW = sizeof(T) == 4 ? D : 64;  // channels of a staged row
+    const float s2 = sinv * qsc.y;
     float bad = 0.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -761,14 +807,13 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const float y1 = __uint_as_float(o1[j + f]), y2 = __uint_as_float(o2[j + f]);
-          const float x = F16 ? fmaf(ev[f], y2 * sinv, y1 * pv[f]) : fmaf(ev[f], y2, y1);
+          const float x = F16 ? fmaf(ev[f], y2 * s2, y1 * (F32 ? pv[f] * vsc.y : pv[f])) : fmaf(ev[f], y2, y1);
           bad = fmaf(x, 0.f, bad);
           stage[(row / SW) * CH * SW + (t + f) * SW + row % SW] = from_f32<T>(x);
         }
       }
     }
-    lq.put(sm + L::Q);
-    lk.put(sm + L::K);
+    if (F32 && more) write_max();
     fence_proxy_async_smem();
     tc_fence_before_sync();
     // a sum of zeros unless a value is not finite (one of the rows past the chunk's tokens, then,
@@ -776,7 +821,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     const bool redo = __syncthreads_or(bad != 0.f && row < a.dv);
     tc_fence_after_sync();
     // the next chunk's scores may take O1's place: its q and k have come meanwhile
-    if (more) issue_scores(ph ^ 1);
+    if (!F32 && more) issue_scores(ph ^ 1);
+    const float ainv = kscale.y * vsc.y;
+    if (more) put_qk();
     if (redo) {
       token_by_token(t0, n, d);
     } else {
@@ -795,7 +842,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
                 *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(stage) + i * 16);
         }
       }
-      add_state(d->lam, kscale.y);
+      add_state(d->lam, ainv);
     }
     put_state();
     if (NP == 1 && iwarp && elect_one()) {
@@ -951,7 +998,7 @@ cudaError_t linattn_chunk_launch(const LinattnArgs& a, int type, void* ws, bool 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool wide = a.dk > 112;
   if (type == MOE_F32)
-    return wide ? chunk_launch<float, 3, true>(a, type, w, pdl, st) : chunk_launch<float, 3, false>(a, type, w, pdl, st);
+    return wide ? chunk_launch<float, 2, true>(a, type, w, pdl, st) : chunk_launch<float, 2, false>(a, type, w, pdl, st);
   if (type == MOE_F16)
     return wide ? chunk_launch<__half, 1, true>(a, type, w, pdl, st) : chunk_launch<__half, 1, false>(a, type, w, pdl, st);
   return wide ? chunk_launch<__nv_bfloat16, 1, true>(a, type, w, pdl, st)

@@ -244,6 +244,26 @@ def test_non_finite_does_not_reach_back(type, bad, where):
         assert not torch.isfinite(o[t:200, 1]).any()
 
 
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_value_early_in_a_long_prompt(type, bad):
+    """A value of v that is not finite near the start of a prompt that is cut into several units
+    keeps to its channel all the way, outputs and state."""
+    c = Case([700, 130], H=2, dk=128, dv=128, type=type, decay="head")
+    c.v[65, 1, 5] = 0
+    want = c.want()
+    c.v[65, 1, 5] = bad
+    o = c.prefill()
+    ok = torch.ones(830, 2, 128, dtype=torch.bool, device="cuda")
+    ok[65:700, 1, 5] = False
+    oks = torch.ones(2, 2, 128, 128, dtype=torch.bool, device="cuda")
+    oks[0, 1, :, 5] = False
+    assert not torch.isfinite(o[65:700, 1, 5]).any() and not torch.isfinite(c.state[0, 1, :, 5]).any()
+    m, ms = ok.cpu().numpy(), oks.cpu().numpy()
+    c.check(torch.where(ok, o, 0), torch.where(oks, c.state, 0),
+            tuple(np.where(x, w, 0) for x, w in zip((m, ms, m, ms), want)))
+
+
 def test_fresh_state_ignores_what_was_there():
     c = Case([80, 0, 30], dk=64, dv=64, type="bf16", fresh=True)
     want = c.want()
