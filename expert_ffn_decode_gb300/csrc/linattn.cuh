@@ -36,7 +36,7 @@ constexpr int UNIT_SCRATCH = 4 + 3 * 8;  // ints of shared memory that find_unit
 // Unit u of the call: u < B are the last (or only) units of the sequences, u >= B counts the
 // others, each of seg tokens, in sequence order. Of up to 256 sequences the last units of more
 // than half of seg come first, so that a grid in this order ends with its shortest pieces. A
-// whole CTA of 256 threads adds up what the sequences before it have. `n_ws`: states in the
+// whole CTA (256 threads of it) adds up what the sequences before it have. `n_ws`: states in the
 // workspace; a sequence whose units would not fit (offsets that descend can make sequences
 // share tokens) is not found.
 __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_ws, int u, int* scratch) {
@@ -54,7 +54,7 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_w
   int base_u = 0, base_s = 0;
   if (tid == 0) scratch[0] = -1;
   for (int b0 = 0; b0 < a.B; b0 += 256) {
-    const int b = b0 + tid;
+    const int b = tid < 256 ? b0 + tid : a.B;
     int ns = 0, tail = 0;
     if (b < a.B) {
       int begin, end;
@@ -77,7 +77,7 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_w
       }
     }
     __syncthreads();  // the last round's sums have been read
-    if (lane == 31) {
+    if (lane == 31 && warp < 8) {
       scratch[4 + 3 * warp] = cu;
       scratch[5 + 3 * warp] = cs;
       scratch[6 + 3 * warp] = cl;

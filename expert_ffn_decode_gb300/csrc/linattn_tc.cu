@@ -46,7 +46,7 @@ struct Plan {
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
   static constexpr uint32_t P = KT + (NP == 1 ? 3 : 2) * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
-  static constexpr uint32_t BYTES = MISC + 5760;  // NP 1: 114,304 bytes and 1,024 of slack, two CTAs an SM
+  static constexpr uint32_t BYTES = MISC + (NP == 1 ? 6016 : 7424);  // NP 1: 114,560 bytes and 1,024 of slack, two CTAs an SM
   // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
   // their place once O2 is done (a thread's columns of A are its columns of the parts).
   static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128, T_COLS = 256;
@@ -64,6 +64,7 @@ struct Decays {
   float wmax;        // largest w
   int pad[2];
 };
+template <int NWG>  // warpgroups
 struct Misc {
   Decays d[2];       // of this chunk and the next
   uint64_t full_q, full_k, full_v;  // a tile has landed
@@ -72,9 +73,9 @@ struct Misc {
   int scratch[UNIT_SCRATCH];
   // f16: largest magnitudes on the way to the scales, and the scores' inverse scales
   alignas(16) float pinv[CH];
-  float kmax[8], smax[2][128], pmax[2][32], tmax[3][8];  // tmax: f32 q, k, v by warp
+  float kmax[8], smax[NWG][128], pmax[NWG][64], tmax[3][NWG * 4];  // tmax: f32 q, k, v by warp
 };
-static_assert(sizeof(Misc) <= 5760, "misc");
+
 
 // bf16 (or f16) operands, K-major (0) or MN-major (1), f32 accumulator, shape M x N.
 template <bool F16>
@@ -184,17 +185,24 @@ __device__ __forceinline__ float2 f16_scale(float mx) {
 // along K, 128 along rows) and as an MN-major one (rows along K: 128 along K, 1024 along columns).
 __device__ __forceinline__ uint32_t piece(int kc, int row) { return (uint32_t)(kc * CH + row) * 16u; }
 
-// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] f32 matrix: four
+// Tiles are shared out by turns of a warp: 8 rows x 32 columns, 8 columns a lane. A warp's turns
+// are `pieces` neighbours in the rows of its number modulo 8 (two warps share them when
+// there are sixteen).
+__device__ __forceinline__ int piece_row() { return (threadIdx.x >> 5 & 7) * 8 + (threadIdx.x & 7); }
+template <int pieces>
+__device__ __forceinline__ int piece_col(int i) { return ((threadIdx.x >> 8) * pieces + i) * 4; }
+
+// A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] f32 matrix:
 // 8-column pieces of one row, fetched early and put into the tile as two f16 parts when that
 // is free. A warp's 32 pieces of one i fill four whole 128-byte lines.
-template <int NP>
+template <int NP, int PIECES>
 struct Loader {
-  float r[NP == 1 ? 1 : D / 32][8];
+  float r[NP == 1 ? 1 : PIECES][8];
   __device__ __forceinline__ void fetch(const float* src, int64_t stride, int t0, int n, int dim) {
-    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+    const int lane = threadIdx.x & 31, row = piece_row(), kc0 = piece_col<PIECES>(0) + (lane >> 3);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int kc = i * 4 + (lane >> 3);
+    for (int i = 0; i < PIECES; ++i) {
+      const int kc = kc0 + i * 4;
       const bool in = row < n && kc * 8 < dim;
       const float* p = in ? src + (t0 + row) * stride + kc * 8 : src;
 #pragma unroll
@@ -212,14 +220,14 @@ struct Loader {
   __device__ __forceinline__ float warp_max() const {
     float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < PIECES; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(r[i][j]));
     mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
     if (mx > 3.402823466e38f) {
       mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+      for (int i = 0; i < PIECES; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = isfinite(r[i][j]) ? fmaxf(mx, fabsf(r[i][j])) : mx;
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
@@ -227,13 +235,13 @@ struct Loader {
     return mx;
   }
   __device__ __forceinline__ void put(uint8_t* dst, float scale) const {
-    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) * 8 + (lane & 7);
+    const int lane = threadIdx.x & 31, row = piece_row(), kc0 = piece_col<PIECES>(0) + (lane >> 3);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < PIECES; ++i) {
       uint32_t u[4][NP];
 #pragma unroll
       for (int j = 0; j < 4; ++j) split_pair<NP, true>(r[i][2 * j] * scale, r[i][2 * j + 1] * scale, u[j]);
-      uint8_t* d = dst + piece(i * 4 + (lane >> 3), row);
+      uint8_t* d = dst + piece(kc0 + i * 4, row);
 #pragma unroll
       for (int q = 0; q < NP; ++q)
         *reinterpret_cast<uint4*>(d + q * TILE) = make_uint4(u[0][q], u[1][q], u[2][q], u[3][q]);
@@ -352,6 +360,8 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
   }
 }
 
+// f32 takes one CTA an SM, of sixteen warps.
+constexpr int chunk_threads(int np) { return np == 1 ? 256 : 512; }
 struct Maps {
   CUtensorMap q, k, v, o;  // 16-bit types only
 };
@@ -369,16 +379,20 @@ struct Maps {
 //   left it.
 // Two bf16 CTAs share an SM, so one's products run beside the other's arithmetic.
 template <typename T, int NP, int MODE, bool WIDE>
-__global__ void __launch_bounds__(256, NP == 1 ? 2 : 1)
+__global__ void __launch_bounds__(chunk_threads(NP), NP == 1 ? 2 : 1)
 lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
   using L = Plan<NP>;
+  static_assert(sizeof(Misc<chunk_threads(NP) / 128>) <= L::BYTES - L::MISC, "misc");
   constexpr bool F16 = !std::is_same<T, __nv_bfloat16>::value;  // the type of the parts
   constexpr bool F32 = std::is_same<T, float>::value;
   constexpr int NPP = L::NPP, LIM = 1;  // products of parts i, j with i + j <= LIM
   constexpr int KP = F16 ? 2 : 3;       // parts of the decayed keys
+  constexpr int NT = chunk_threads(NP), NWG = NT / 128;  // threads; warpgroups, which share rows
+  constexpr int CPT = D / NWG, TPT = CH / NWG, SPT = 4 / NWG;  // a thread's columns of S, tokens, mask steps
+  constexpr int PIECES = 8 / NWG;                              // a warp's turns through a tile
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
-  Misc* m = reinterpret_cast<Misc*>(sm + L::MISC);
+  auto* m = reinterpret_cast<Misc<NWG>*>(sm + L::MISC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, quarter = warp & 3;
   const bool iwarp = __shfl_sync(0xffffffffu, warp, 0) == 3;  // whose elected lane issues
   // The heads of a unit are neighbours. Whole units come first and the sequences' last ones,
@@ -399,7 +413,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   T* o = static_cast<T*>(a.o) + (int64_t)h * a.dv;
   if (slot < 0) {
     if (MODE == 1)
-      for (int i = tid; i < (end - begin) * a.dv; i += 256)
+      for (int i = tid; i < (end - begin) * a.dv; i += NT)
         o[(begin + i / a.dv) * a.os + i % a.dv] = from_f32<T>(0.f);
     return;
   }
@@ -418,7 +432,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   tc_fence_after_sync();
   const uint32_t tm = __shfl_sync(0xffffffffu, m->tmem, 0), tlane = tm + ((uint32_t)quarter * 32u << 16);
   const int hq = h / a.rep, ks = WIDE ? D / 16 : (a.dk + 15) / 16;  // steps of 16 along the keys' width
-  const bool cols = WIDE || wg * 64 < a.dk;                 // whether this thread's half of S^T has columns
+  const bool cols = WIDE || wg * CPT < a.dk;                // whether this thread's part of S^T has columns
   const T* q = static_cast<const T*>(a.q) + (int64_t)hq * a.dk;
   const T* k = static_cast<const T*>(a.k) + (int64_t)hq * a.dk;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
@@ -432,7 +446,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     tma_load_tile(sm + L::V, &maps.v, a.dv, h, begin, &m->full_v);
   }
   // f32: a chunk's q, k and v on their way, and the scales (and their inverses) of their tiles
-  Loader<NP> lq, lk, lv;
+  Loader<NP, PIECES> lq, lk, lv;
   float2 qsc = make_float2(1.f, 1.f), ksc = qsc, vsc = qsc;
   float kmx = 0.f;
   auto fetch = [&](int t0) {
@@ -455,7 +469,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
 #pragma unroll
       for (int i = 0; i < 3; ++i)
 #pragma unroll
-        for (int w = 0; w < 8; ++w) mx[i] = fmaxf(mx[i], m->tmax[i][w]);
+        for (int w = 0; w < NT / 32; ++w) mx[i] = fmaxf(mx[i], m->tmax[i][w]);
       qsc = f16_scale(mx[0]);
       ksc = f16_scale(mx[1]);
       vsc = f16_scale(mx[2]);
@@ -472,14 +486,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   }
   if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
 
-  // S^T: this thread's row, key columns 64 wg .. 64 wg + 63
-  float S[64];
+  // S^T: this thread's row, CPT key columns from CPT wg on
+  float S[CPT];
   {
     const float* from = un.n > 1 ? mine : pool;
     const bool zero = MODE == 0 || (un.n == 1 && a.fresh);
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-      S[j] = !zero && row < a.dv && wg * 64 + j < a.dk ? from[(wg * 64 + j) * a.dv + row] : 0.f;
+    for (int j = 0; j < CPT; ++j)
+      S[j] = !zero && row < a.dv && wg * CPT + j < a.dk ? from[(wg * CPT + j) * a.dv + row] : 0.f;
   }
   float sinv = 1.f;  // f16: inverse scale of this row of the operand
   auto put_state = [&]() {  // the state's parts as an operand in tensor memory
@@ -487,16 +501,18 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     if constexpr (F16) {
       float mx = 0.f;
 #pragma unroll
-      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, fabsf(S[j]));
+      for (int j = 0; j < CPT; ++j) mx = fmaxf(mx, fabsf(S[j]));
       m->smax[wg][row] = mx;
       __syncthreads();
-      const float2 f = f16_scale(fmaxf(mx, m->smax[wg ^ 1][row]));
+#pragma unroll
+      for (int i = 1; i < NWG; ++i) mx = fmaxf(mx, m->smax[(wg + i) % NWG][row]);
+      const float2 f = f16_scale(mx);
       sc = f.x;
       sinv = f.y;
     }
     if (cols) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < CPT / 32; ++c) {
         uint32_t u[NPP][16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -506,7 +522,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
           for (int p = 0; p < NPP; ++p) u[p][j] = s[p];
         }
 #pragma unroll
-        for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + (wg * NPP + p) * 32 + c * 16, u[p]);
+        for (int p = 0; p < NPP; ++p) tmem_st16(tlane + L::T_S + (wg * NPP + p) * (CPT / 2) + c * 16, u[p]);
       }
       tmem_st_wait();
     }
@@ -514,10 +530,10 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   auto add_state = [&](float lam, float ainv) {  // S = lam S + A
     if (cols) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (wg * 4 + c >= ks) break;  // columns that A does not have
+      for (int c = 0; c < CPT / 16; ++c) {
+        if (wg * (CPT / 16) + c >= ks) break;  // columns that A does not have
         uint32_t r[16];
-        tmem_ld16(tlane + L::T_A + wg * 64 + c * 16, r);
+        tmem_ld16(tlane + L::T_A + wg * CPT + c * 16, r);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -537,8 +553,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       const float lam = d->g[t].w;
       float acc = 0.f;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const int at = wg * 64 + c * 4;
+      for (int c = 0; c < CPT / 4; ++c) {
+        const int at = wg * CPT + c * 4;
         if (at < a.dk) {
           const float4 kk = load4(k + (t0 + t) * a.ks + at), qq = load4(q + (t0 + t) * a.qs + at);
           const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, q4[4] = {qq.x, qq.y, qq.z, qq.w};
@@ -549,9 +565,13 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
           }
         }
       }
-      if (wg == 1) part[row] = acc;
+      if (wg > 0) part[wg * 128 + row] = acc;
       __syncthreads();
-      if (wg == 0 && row < a.dv) o[(t0 + t) * a.os + row] = from_f32<T>((acc + part[row]) * a.scale);
+      if (wg == 0 && row < a.dv) {
+#pragma unroll
+        for (int i = 1; i < NWG; ++i) acc += part[i * 128 + row];
+        o[(t0 + t) * a.os + row] = from_f32<T>(acc * a.scale);
+      }
       __syncthreads();
     }
     fence_proxy_async_smem();
@@ -598,8 +618,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       auto largest = [&](auto keep) {
         uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
+        for (int i = 0; i < PIECES; ++i) {
+          const int r = piece_row(), kc = piece_col<PIECES>(i) + (lane >> 3);
           if (r < n && kc < 2 * ks) {
             const uint4 u = *reinterpret_cast<const uint4*>(sm + L::K + tile_piece<NP>(kc, r));
             mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(keep(u.x & 0x7fff7fffu), keep(u.y & 0x7fff7fffu)),
@@ -618,9 +638,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       kscale = f16_scale(km * d->wmax);
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int r = warp * 8 + (lane & 7), kc = i * 4 + (lane >> 3);
-      if (i * 4 >= 2 * ks) break;
+    for (int i = 0; i < PIECES; ++i) {
+      const int r = piece_row(), kc = piece_col<PIECES>(i) + (lane >> 3);
+      if (piece_col<PIECES>(i) >= 2 * ks) break;
       const float w = d->w[r] * kscale.x * ksc.y;
       float x[8];
       read_piece<NP, F16>(sm + L::K + tile_piece<NP>(kc, r), x);
@@ -637,7 +657,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     }
     if (NP == 1 && n < CH) {
       ok = mbar_wait(&m->full_v, ph) && ok;
-      for (int i = n * 16 + tid; i < CH * 16; i += 256)
+      for (int i = n * 16 + tid; i < CH * 16; i += NT)
         *reinterpret_cast<uint4*>(tv + tile_piece<1>(i & 15, i >> 4)) = make_uint4(0, 0, 0, 0);
     }
     sum_lo += d->glo;
@@ -660,7 +680,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     if (iwarp && elect_one()) {
       if (MODE == 1) {
         each_product<NPP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
-          mma_ts(tm + L::T_O2, tm + L::T_S + (s / 4 * NPP + i) * 32 + s % 4 * 8, desc_k<NP>(sm + L::Q + j * TILE, s),
+          mma_ts(tm + L::T_O2, tm + L::T_S + (s * 16 / CPT * NPP + i) * (CPT / 2) + s * 16 % CPT / 2, desc_k<NP>(sm + L::Q + j * TILE, s),
                  idesc<F16>(128, CH, 0, 0), !first);
         });
         mma_commit(&m->qs);
@@ -681,18 +701,18 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     }
     __syncwarp();
     // ---- masked scores and the chunk's own share -----------------------------------------
-    if (MODE == 1 && quarter < 2 && wg <= quarter) {
-      // Lanes 0 .. 63 hold the tokens' rows of scores; columns 32 wg .. 32 wg + 31 here, of
-      // which the mask leaves none for rows below 32 and wg 1.
+    if (MODE == 1 && quarter < 2 && wg * SPT < 2 * (quarter + 1)) {
+      // Lanes 0 .. 63 hold the tokens' rows of scores; a thread takes SPT steps of 16 columns. The
+      // mask leaves rows below 32 none of the last two steps.
       ok = mbar_wait(&m->qk, ph) && ok;
       tc_fence_after_sync();
       const float4 gt = d->g[row];
       const float qk = qsc.y * ksc.y, et = d->eg[row];
-      uint32_t sc[2][16];
+      uint32_t sc[SPT][16];
       float mx = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int step = wg * 2 + c;  // of the product over s
+      for (int c = 0; c < SPT; ++c) {
+        const int step = wg * SPT + c;  // of the product over s
         uint32_t (&s)[16] = sc[c];
         tmem_ld16(tlane + L::T_O1 + step * 16, s);
         tmem_ld_wait();
@@ -715,7 +735,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
             s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * qk * x * a.scale) : 0u;
           }
         }
-        if (wg == quarter) {  // (rows 32 .. 63 see all of the first 32 columns)
+        if (step >= 2 * quarter) {  // (rows 32 .. 63 see all of the first 32 columns)
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = step * 16 + j <= row ? s[j] : 0u;
         }
@@ -725,19 +745,19 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
         }
       }
       float rs = 1.f;
-      if constexpr (F16) {  // rows 32 .. 63 are two threads'
-        if (quarter == 1) {
-          m->pmax[wg][lane] = mx;
-          asm volatile("bar.sync 2, 64;" ::: "memory");
-          mx = fmaxf(mx, m->pmax[wg ^ 1][lane]);
+      if constexpr (F16) {  // a row's threads are in (quarter + 1) NWG / 2 warps
+        if (NWG == 4 || quarter == 1) {
+          m->pmax[wg][row] = mx;
+          asm volatile("bar.sync %0, %1;" ::"r"(2 + quarter), "r"((quarter + 1) * NWG * 16) : "memory");
+          for (int i = 0; i < (quarter + 1) * NWG / 2; ++i) mx = fmaxf(mx, m->pmax[i][row]);
         }
         const float2 f = f16_scale(mx);
         rs = f.x;
         if (wg == 0) m->pinv[row] = f.y;
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int step = wg * 2 + c;
+      for (int c = 0; c < SPT; ++c) {
+        const int step = wg * SPT + c;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t u[4][NPP];
@@ -757,10 +777,10 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
       }
       fence_proxy_async_smem();
       tc_fence_before_sync();
-      asm volatile("bar.arrive 1, 128;" ::: "memory");  // three warps of scores and the issuer's
+      asm volatile("bar.arrive 1, %0;" ::"n"(NWG * 48 + 32) : "memory");  // the warps of scores and the issuer's
     }
     if (MODE == 1 && iwarp) {
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(NWG * 48 + 32) : "memory");
       tc_fence_after_sync();
       if (elect_one()) {
         each_product<NP, NPP, LIM, CH / 16>(CH / 16, [&](int i, int j, int s, bool first) {
@@ -789,14 +809,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     const float s2 = sinv * qsc.y;
     float bad = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < TPT / 16; ++c) {
       uint32_t o1[16], o2[16];
-      tmem_ld16(tlane + L::T_O1 + wg * 32 + c * 16, o1);
-      tmem_ld16(tlane + L::T_O2 + wg * 32 + c * 16, o2);
+      tmem_ld16(tlane + L::T_O1 + wg * TPT + c * 16, o1);
+      tmem_ld16(tlane + L::T_O2 + wg * TPT + c * 16, o2);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
-        const int t = wg * 32 + c * 16 + j;
+        const int t = wg * TPT + c * 16 + j;
         const float4 e = *reinterpret_cast<const float4*>(&d->eg[t]);
         const float ev[4] = {e.x, e.y, e.z, e.w};
         float pv[4] = {1.f, 1.f, 1.f, 1.f};
@@ -835,7 +855,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
         }
       } else {
         constexpr int PC = SW * (int)sizeof(T) / 16;  // 16-byte pieces of a staged row
-        for (int i = tid; i < CH * (D / SW) * PC; i += 256) {
+        for (int i = tid; i < CH * (D / SW) * PC; i += NT) {
           const int t = i / PC % CH, c = i / PC / CH * SW + i % PC * (16 / (int)sizeof(T));
           if (t < n && c < a.dv)
             *reinterpret_cast<uint4*>(o + (t0 + t) * a.os + c) =
@@ -862,8 +882,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   float* to = MODE == 0 ? mine + (int64_t)a.H * sz : pool;  // what a unit leaves is the next one's start
   if (ok && (MODE == 0 || end == last)) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-      if (row < a.dv && wg * 64 + j < a.dk) to[(wg * 64 + j) * a.dv + row] = S[j];
+    for (int j = 0; j < CPT; ++j)
+      if (row < a.dv && wg * CPT + j < a.dk) to[(wg * CPT + j) * a.dv + row] = S[j];
   }
   if (MODE == 0 && tid == 0) wd[(int64_t)(un.slot0 + un.i) * a.H + h] = resets ? 0.f : ex2(sum_hi + sum_lo);
   if (NP == 1 && MODE == 1 && iwarp && elect_one()) store_wait_all();
@@ -924,12 +944,12 @@ __global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws
 }
 
 template <typename K, typename... Args>
-cudaError_t launch(K kern, dim3 grid, int smem, bool pdl, cudaStream_t st, Args... args) {
+cudaError_t launch(K kern, dim3 grid, int threads, int smem, bool pdl, cudaStream_t st, Args... args) {
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -980,15 +1000,15 @@ cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, 
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
   const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.seg * a.B;  // units but the last, at most
   if (whole > 0) {
-    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst,
+    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst,
                ctrl);
     if (e != cudaSuccess) return e;
     const int by_seq = a.B <= whole;
     const dim3 jgrid((unsigned)(by_seq ? a.B : whole), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
-    e = launch(lin_join, jgrid, 0, pdl, st, a, sp.seg, sp.n_ws, by_seq, (const float*)wd, wst);
+    e = launch(lin_join, jgrid, 256, 0, pdl, st, a, sp.seg, sp.n_ws, by_seq, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
+  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
                 wd, wst, ctrl);
 }
 
