@@ -11,7 +11,7 @@
 //   A^T [dv][dk] = V^T (exp(G_63 - G_s) K)    what the chunk adds to the state
 // The outputs and the state are held transposed, dv on the tensor memory's lanes: then V^T
 // is one operand for two products, S^T comes from tensor memory without a pass through
-// shared memory, and a thread owns half a row of S^T in f32 registers.
+// shared memory, and a thread owns a piece of a row of S^T in f32 registers.
 //
 // Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; an
 // f32 one becomes two f16 parts (22 bits) of its value times a power of two for the chunk's
@@ -46,7 +46,8 @@ struct Plan {
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
   static constexpr uint32_t P = KT + (NP == 1 ? 3 : 2) * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
-  static constexpr uint32_t BYTES = MISC + (NP == 1 ? 6016 : 7424);  // NP 1: 114,560 bytes and 1,024 of slack, two CTAs an SM
+  // NP 1: 114,560 bytes and 1,024 of slack, two CTAs an SM
+  static constexpr uint32_t BYTES = MISC + (NP == 1 ? 6016 : 7424);
   // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
   // their place once O2 is done (a thread's columns of A are its columns of the parts).
   static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128, T_COLS = 256;
@@ -75,7 +76,6 @@ struct Misc {
   alignas(16) float pinv[CH];
   float kmax[8], smax[NWG][128], pmax[NWG][64], tmax[3][NWG * 4];  // tmax: f32 q, k, v by warp
 };
-
 
 // bf16 (or f16) operands, K-major (0) or MN-major (1), f32 accumulator, shape M x N.
 template <bool F16>
@@ -112,7 +112,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Operand descriptors of a [64][128] tile, for step s of 16 along K. A tile of one bf16 part
+// Operand descriptors of a [64][128] tile, for step s of 16 along K. A tile of one part
 // comes by TMA as two halves of 64 columns, rows of 128 bytes in the 128-byte swizzle; tiles of
 // several parts and the decayed keys are written by threads as core matrices without one.
 __device__ __forceinline__ uint64_t desc_sw128(const uint8_t* p, uint32_t lbo) {
@@ -377,10 +377,12 @@ struct Maps {
 //   QS, KV while the scores are masked | PV | the next chunk's QK while the state is updated;
 //   the next k after QK, q after QS, v after the outputs, which are turned in v's place, have
 //   left it.
-// Two bf16 CTAs share an SM, so one's products run beside the other's arithmetic.
+// Two CTAs share an SM for 16-bit types, so one's products run beside the other's arithmetic;
+// f32 has one of sixteen warps, and its products of a chunk start when its tiles are written.
 template <typename T, int NP, int MODE, bool WIDE>
 __global__ void __launch_bounds__(chunk_threads(NP), NP == 1 ? 2 : 1)
-lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, float* wd, float* wst, uint32_t* ctrl) {
+lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, int behind_join, float* wd, float* wst,
+          uint32_t* ctrl) {
   using L = Plan<NP>;
   static_assert(sizeof(Misc<chunk_threads(NP) / 128>) <= L::BYTES - L::MISC, "misc");
   constexpr bool F16 = !std::is_same<T, __nv_bfloat16>::value;  // the type of the parts
@@ -401,9 +403,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   const int h = blockIdx.x % a.H, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
   const int whole = (int)(gridDim.x / a.H) - a.B, at = blockIdx.x / a.H;  // MODE 1: units but the last, at most
   const int u = MODE == 0 || at < whole ? a.B + at : at - whole;
-  pdl_wait_prior_grids();
+  // Behind the join everything but the states is older than the state pass, which has ended: this
+  // grid then sets up and loads its first chunk beside the join and waits for the states alone.
+  if (!behind_join) pdl_wait_prior_grids();
   const Unit un = find_unit(a, seg, n_ws, u, m->scratch);
-  if (!un.found) return;
+  if (!un.found) {
+    if (behind_join) pdl_wait_prior_grids();  // no grid ends before the one it stands behind
+    return;
+  }
   int begin, end;
   seq_range(a, un.b, begin, end);
   const int last = end;
@@ -412,6 +419,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   const int slot = seq_slot(a, un.b);
   T* o = static_cast<T*>(a.o) + (int64_t)h * a.dv;
   if (slot < 0) {
+    if (behind_join) pdl_wait_prior_grids();
     if (MODE == 1)
       for (int i = tid; i < (end - begin) * a.dv; i += NT)
         o[(begin + i / a.dv) * a.os + i % a.dv] = from_f32<T>(0.f);
@@ -486,6 +494,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
   }
   if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
 
+  if (behind_join) pdl_wait_prior_grids();
   // S^T: this thread's row, CPT key columns from CPT wg on
   float S[CPT];
   {
@@ -680,8 +689,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, f
     if (iwarp && elect_one()) {
       if (MODE == 1) {
         each_product<NPP, NP, LIM, D / 16>(ks, [&](int i, int j, int s, bool first) {
-          mma_ts(tm + L::T_O2, tm + L::T_S + (s * 16 / CPT * NPP + i) * (CPT / 2) + s * 16 % CPT / 2, desc_k<NP>(sm + L::Q + j * TILE, s),
-                 idesc<F16>(128, CH, 0, 0), !first);
+          mma_ts(tm + L::T_O2, tm + L::T_S + (s * 16 / CPT * NPP + i) * (CPT / 2) + s * 16 % CPT / 2,
+                 desc_k<NP>(sm + L::Q + j * TILE, s), idesc<F16>(128, CH, 0, 0), !first);
         });
         mma_commit(&m->qs);
         ok = mbar_wait(&m->qk, ph) && ok;
@@ -900,6 +909,7 @@ __global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws
                                                 float* wst) {
   __shared__ int scratch[UNIT_SCRATCH];
   pdl_wait_prior_grids();
+  pdl_launch_dependents();  // the output pass may set up
   const Unit un = find_unit(a, seg, n_ws, by_seq ? blockIdx.x : a.B + blockIdx.x, scratch);
   if (!un.found || un.n == 1 || (!by_seq && un.i != 0)) return;
   const int slot = seq_slot(a, un.b);
@@ -1000,8 +1010,8 @@ cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, 
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
   const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.seg * a.B;  // units but the last, at most
   if (whole > 0) {
-    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws, wd, wst,
-               ctrl);
+    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws, 0, wd,
+               wst, ctrl);
     if (e != cudaSuccess) return e;
     const int by_seq = a.B <= whole;
     const dim3 jgrid((unsigned)(by_seq ? a.B : whole), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
@@ -1009,7 +1019,7 @@ cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, 
     if (e != cudaSuccess) return e;
   }
   return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
-                wd, wst, ctrl);
+                whole > 0 ? 1 : 0, wd, wst, ctrl);
 }
 
 }  // namespace
