@@ -264,6 +264,49 @@ def test_non_finite_value_early_in_a_long_prompt(type, bad):
             tuple(np.where(x, w, 0) for x, w in zip((m, ms, m, ms), want)))
 
 
+@pytest.mark.parametrize("type", list(TYPES))
+def test_many_sequences_few_of_them_long(type):
+    """More sequences than a CTA counts in one go, some cut into units, some empty or inactive."""
+    rng = np.random.default_rng(12)
+    lens = [int(n) for n in rng.integers(0, 4, 300)]
+    for b, n in ((3, 513), (70, 300), (255, 140), (256, 129), (290, 128), (299, 400)):
+        lens[b] = n
+    slots = [int(x) for x in rng.permutation(310)[:300]]
+    for b in (5, 70, 120, 290):
+        slots[b] = -1 - b
+    c = Case(lens, H=2, G=1, dk=64, dv=32, type=type, decay="reset", n_states=310, slots=slots)
+    want = c.want()
+    c.check(c.prefill(), c.state, want)
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("lens,H", [([450, 450], 2), ([1300], 30), ([700, 60, 500], 24)])
+def test_long_prompts(lens, H, type):
+    """Prompts of several units, with few and with many heads, with and without offsets."""
+    c = Case(lens, H=H, G=H // 2, dk=128, dv=64, type=type, decay="token")
+    first = c.state.clone()
+    want = c.want()
+    c.check(c.prefill(), c.state, want)
+    if len(set(lens)) == 1:
+        c.state.copy_(first)
+        c.check(c.prefill(offsets=None), c.state, want)
+
+
+def test_one_workspace_for_calls_of_any_size():
+    """A workspace that other calls have used gives what a fresh one gives."""
+    ws = None
+    for lens, H, type in (([900, 200], 4, "bf16"), ([500], 2, "f32"), ([2000], 3, "f16"), ([900, 200], 4, "bf16")):
+        c = Case(lens, H=H, dk=128, dv=128, type=type)
+        want, cfg = c.want(), c.cfg()
+        if ws is None:
+            ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+        o = torch.empty(sum(lens), H, 128, dtype=TYPES[type][1], device="cuda")
+        st = torch.cuda.current_stream()
+        ffn.check(ffn.moe_linattn_prefill(c.q, c.k, c.v, c.g, c.offsets, None, cfg, c.state, o, ws, ws.numel(), st))
+        ffn.check(ffn.moe_workspace_status(ws, st))
+        c.check(o, c.state, want)
+
+
 def test_fresh_state_ignores_what_was_there():
     c = Case([80, 0, 30], dk=64, dv=64, type="bf16", fresh=True)
     want = c.want()

@@ -126,6 +126,16 @@ def test_workspace_size(built):
     assert n >= 512 and n % 256 == 0
 
 
+def test_workspace_holds_every_units_state(built):
+    """A prompt that is cut needs a state for each unit of each head; one that stays whole none."""
+    small = ffn.moe_linattn_workspace_size(la_cfg(n_seq=1, n_tokens=200))
+    large = ffn.moe_linattn_workspace_size(la_cfg(n_seq=1, n_tokens=4096))
+    assert small == 512
+    units = -(-4096 // 128)  # at most this many: units have at least 128 tokens
+    state = 4 * 64 * 128 * 4
+    assert 512 + 2 * state < large <= 2 * units * (state + 64) + 1024
+
+
 @pytest.mark.parametrize("qtype", [oo.Q4_0, oo.Q4_1, oo.Q4_K])
 def test_oracle_blocks_against_the_steps(qtype):
     """The oracle's (q, scale, offset) give the values of the step's pinned decoders."""
