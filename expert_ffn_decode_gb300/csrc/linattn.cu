@@ -13,8 +13,8 @@ namespace {
 // is a stream of the states (128 KB a head) and bound by it. 256 threads take COLS * 4 value
 // columns of one head: a thread owns 4 neighbouring columns of every GROUPS-th run of rows, so
 // a warp's load is whole lines, all of a thread's loads are in flight together, and the
-// outputs are joined over the row groups in order. COLS 32 is a whole head; calls with few
-// heads take 8 (four CTAs a head), so that one sequence already spreads over the GPU.
+// outputs are joined over the row groups in order. COLS 32 or 16 is a whole head; calls with
+// few heads take 8 (up to four CTAs a head), so that one sequence already spreads over the GPU.
 template <typename T, int COLS>
 __global__ void __launch_bounds__(256) lin_step(LinattnArgs a) {
   constexpr int GROUPS = 256 / COLS, ROWS = 128 / GROUPS;
@@ -189,8 +189,11 @@ cudaError_t scan_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
 
 template <typename T>
 cudaError_t step_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
-  if ((int64_t)a.B * a.H >= 304)  // as many CTAs as two an SM
-    return launch(lin_step<T, 32>, dim3(1, (unsigned)a.H, (unsigned)a.B), 256, pdl, st, a);
+  if ((int64_t)a.B * a.H >= 304) {  // as many CTAs as two an SM: a whole head each
+    const dim3 grid(1, (unsigned)a.H, (unsigned)a.B);
+    if (a.dv > 64) return launch(lin_step<T, 32>, grid, 256, pdl, st, a);
+    if (a.dv > 32) return launch(lin_step<T, 16>, grid, 256, pdl, st, a);
+  }
   return launch(lin_step<T, 8>, dim3((unsigned)((a.dv + 31) / 32), (unsigned)a.H, (unsigned)a.B), 256, pdl, st, a);
 }
 

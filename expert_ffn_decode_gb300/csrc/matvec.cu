@@ -41,15 +41,16 @@ enum { ROW_Q4_0, ROW_Q4_1, ROW_Q4_K, ROW_PLANES };
 // How a call's vectors sit in the mma columns.
 //   MULTI false: one vector, four blocks an mma.
 //   MULTI true: NT tiles of 8 columns of PARTS parts, one block an mma.
-template <bool MULTI_, int NT_, int PARTS_>
+template <bool MULTI_, int NT_, int PARTS_, int WARPS_>
 struct Cols {
   static constexpr bool MULTI = MULTI_;
   static constexpr int NT = NT_, PARTS = PARTS_;
   static constexpr int VECS = MULTI ? 8 * NT / PARTS : 1;
   static constexpr int XBYTES = MULTI ? 16 * NT : 4;  // bytes of x pieces for each of a row's values
   // Warps of a CTA and stages of a warp's ring (all but one in flight). Several vectors' x pieces
-  // leave room for one CTA an SM, which then has sixteen warps to share them.
-  static constexpr int WARPS = MULTI ? 16 : 8, DEPTH = MULTI ? 2 : 4;
+  // leave room for one CTA an SM, which then has sixteen warps to share them (8192 x 2560, eight
+  // vectors: 10.8 us, 12.5 with eight), or eight where longer rows leave no more room.
+  static constexpr int WARPS = WARPS_, DEPTH = MULTI ? 2 : 4;
 };
 
 struct MvArgs {
@@ -584,19 +585,34 @@ cudaError_t launch(MvArgs& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, matvec_kernel<RT, C>, p);
 }
 
+// Launches the form if its shared memory fits.
+template <int RT, class C>
+bool try_launch(MvArgs& p, cudaStream_t st, cudaError_t* e) {
+  if (smem_bytes<RT, C>(p) > MV_SMEM) return false;
+  *e = launch<RT, C>(p, st);
+  return true;
+}
 // The column form of a call. A pass of several vectors reads the weights once for all of
-// them but keeps 16 bytes of x pieces a value (32 for eight f32 vectors); rows too long for
-// that take the vectors one at a time.
+// them, up to sixteen, but keeps x pieces for each: 16 bytes a value for four f32 vectors or
+// eight of 16 bits. Rows too long for that (about 2,000 values for sixteen f32 vectors, 5,000
+// for eight, 10,000 for four; twice that in 16 bits) take fewer vectors a pass, in the end one.
+// (8192 x 2048: sixteen f32 vectors 15.1 us in one pass of eight warps, 16.6 in two of sixteen;
+// sixteen bf16 ones 11.3 and 14.9.)
 template <int RT>
 cudaError_t launch_cols(MvArgs& p, cudaStream_t st) {
-  const bool wide = p.a.x_type == MOE_F32;
-  if (p.a.T > 1 && !wide && smem_bytes<RT, Cols<true, 1, 1>>(p) <= MV_SMEM)
-    return launch<RT, Cols<true, 1, 1>>(p, st);
-  if (p.a.T > 4 && wide && smem_bytes<RT, Cols<true, 2, 2>>(p) <= MV_SMEM)
-    return launch<RT, Cols<true, 2, 2>>(p, st);
-  if (p.a.T > 1 && wide && smem_bytes<RT, Cols<true, 1, 2>>(p) <= MV_SMEM)
-    return launch<RT, Cols<true, 1, 2>>(p, st);
-  return launch<RT, Cols<false, 1, 2>>(p, st);
+  cudaError_t e = cudaSuccess;
+  if (p.a.T > 8 && (p.a.x_type == MOE_F32 ? try_launch<RT, Cols<true, 4, 2, 8>>(p, st, &e)
+                                          : try_launch<RT, Cols<true, 2, 1, 16>>(p, st, &e)))
+    return e;
+  if (p.a.T > 1 && p.a.x_type != MOE_F32) {
+    if (try_launch<RT, Cols<true, 1, 1, 16>>(p, st, &e) || try_launch<RT, Cols<true, 1, 1, 8>>(p, st, &e)) return e;
+  } else if (p.a.T > 1) {
+    if (p.a.T > 4 &&
+        (try_launch<RT, Cols<true, 2, 2, 16>>(p, st, &e) || try_launch<RT, Cols<true, 2, 2, 8>>(p, st, &e)))
+      return e;
+    if (try_launch<RT, Cols<true, 1, 2, 16>>(p, st, &e) || try_launch<RT, Cols<true, 1, 2, 8>>(p, st, &e)) return e;
+  }
+  return launch<RT, Cols<false, 1, 2, 8>>(p, st);
 }
 
 }  // namespace

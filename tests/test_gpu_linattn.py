@@ -148,7 +148,8 @@ def test_prefill(kw, type):
     dict(lens=[1]), dict(lens=[1] * 7, H=10, dk=72, dv=40, n_states=9, slots=[3, 0, -1, 8, 9, 5, 1]),
     dict(lens=[1] * 5, H=4, G=1, dk=128, dv=128, decay="reset", fused=True), dict(lens=[1] * 3, dk=8, dv=120, decay="head"),
     dict(lens=[1] * 2, dk=64, dv=64, fresh=True), dict(lens=[1] * 40, H=16, G=8, dk=128, dv=128, decay="head"),
-    dict(lens=[1] * 3, H=5, dk=104, dv=24, decay="reset"),
+    dict(lens=[1] * 3, H=5, dk=104, dv=24, decay="reset"), dict(lens=[1] * 39, H=8, G=4, dk=72, dv=40, decay="reset"),
+    dict(lens=[1] * 80, H=4, dk=128, dv=32), dict(lens=[1] * 80, H=4, dk=24, dv=64), dict(lens=[1] * 31, H=10, dk=96, dv=88),
 ], ids=lambda d: ",".join(f"{k}={v}" for k, v in d.items() if k != "lens") + f",n={len(d['lens'])}")
 def test_step(kw, type):
     c = Case(type=type, **kw)
