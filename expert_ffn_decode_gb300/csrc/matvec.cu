@@ -5,11 +5,12 @@
 // (Q4_0 and planes without offsets: m = -8 d; Q4_K: d and m are the sub-block's d sc and
 // -dmin mn), so a nibble is used as the integer it is and never rounded. The inner sum runs on
 // the tensor cores by mma.m16n8k16, whose operands are registers: at one vector there is a
-// matrix row of work for one accumulator column, far too little for a tcgen05 tile, and the
-// kernel is bound by the weights' bytes. What mma buys is instructions: a pair of nibbles
-// becomes an f16 operand by one AND (the bits of a nibble in the low bits of an f16 are the
-// subnormal q 2^-24, or 16 q 2^-24 for the high one) and one multiplication by a power of two
-// to q 2^-10; about 1.8 instructions a weight, where an f32 dot takes 2.4. The multiplication is
+// matrix row of work for one accumulator column, far too little for a tcgen05 tile. Bytes are the
+// floor and instructions what is left over it: 128,000 x 2048 Q4_0 and one vector take 33.6 us
+// (66% of HBM's rate; 2.9 instructions a weight, the schedulers 62% busy, half of it nibbles; one
+// warp a row with f32 products 888 us). A pair of nibbles becomes an f16 operand by one AND (the
+// bits of a nibble in the low bits of an f16 are the subnormal q 2^-24, or 16 q 2^-24 for the
+// high one) and one multiplication by a power of two to q 2^-10. The multiplication is
 // needed for the sums, not for the values: a subnormal operand counts in the accumulator's
 // alignment with the exponent of the smallest normal number, and up to ten bits of every
 // product are lost (1.2 times outside the rounding bound beside a value 10^6 times its
@@ -23,7 +24,8 @@
 // Columns of one mma are (vector, part) pairs. A single vector has two of eight: the other six
 // take three more blocks. Lane t of a quad of lanes then holds a whole block's nibbles of its
 // row, and x is zero outside the columns of the lane's own block, so the accumulator's
-// column pair t is block t's sum and each lane applies one block's scale.
+// column pair t is block t's sum and each lane applies one block's scale. Rows of an even number
+// of Q4_0 blocks (36 bytes a pair) need no shifts to bring the 18-byte blocks to whole words.
 #include "common.cuh"
 #include "ops_host.h"
 #include "types.cuh"
@@ -35,8 +37,9 @@ constexpr int MV_PITCH = 176;    // bytes of a staged row: 256 values of the wid
                                  // 48 mod 128 spreads four 20-byte blocks of 8 rows over all banks
 constexpr int MV_SPITCH = 32;    // planes: staged bytes of a row's scales (and of its offsets)
 
-// Types of weight rows, as template values.
-enum { ROW_Q4_0, ROW_Q4_1, ROW_Q4_K, ROW_PLANES };
+// Types of weight rows, as template values (Q4_0_PAIRS: one vector, an even number of blocks a row).
+enum { ROW_Q4_0, ROW_Q4_0_PAIRS, ROW_Q4_1, ROW_Q4_K, ROW_PLANES };
+constexpr bool is_q4_0(int rt) { return rt == ROW_Q4_0 || rt == ROW_Q4_0_PAIRS; }
 
 // How a call's vectors sit in the mma columns.
 //   MULTI false: one vector, four blocks an mma.
@@ -46,6 +49,7 @@ struct Cols {
   static constexpr bool MULTI = MULTI_;
   static constexpr int NT = NT_, PARTS = PARTS_;
   static constexpr int VECS = MULTI ? 8 * NT / PARTS : 1;
+  static constexpr int JOIN = MULTI ? VECS : 2;  // tiles of 16 sums a warp puts up at a time
   static constexpr int XBYTES = MULTI ? 16 * NT : 4;  // bytes of x pieces for each of a row's values
   // Warps of a CTA and stages of a warp's ring (all but one in flight). Several vectors' x pieces
   // leave room for one CTA an SM, which then has sixteen warps to share them (8192 x 2560, eight
@@ -95,6 +99,34 @@ __device__ __forceinline__ void mma_high(float (&c)[4], uint32_t w, uint32_t u, 
   if (first) mma16816_zero(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
   else mma16816(c, high_h2(w), high_h2(u), high_h2(w >> 8), high_h2(u >> 8), b0, b1);
 }
+// Single vector, where the integer pipe is what bounds: the odd bytes' high nibbles are the bytes
+// less their low nibbles, an exact f16 sum instead of a mask. High nibbles come out as
+// q 2^-6 and have an accumulator of their own, h.
+struct Nibbles {
+  uint32_t low[2], high[2];  // even, odd bytes
+};
+__device__ __forceinline__ Nibbles nibbles(uint32_t w) {
+  Nibbles n;
+  const uint32_t odd = __byte_perm(w, 0, 0x4341);
+  n.low[0] = low_h2(w);
+  n.low[1] = low_h2(odd);
+  n.high[0] = mul_h2(w & 0x00f000f0u, 0x74007400u);
+  asm("{ .reg .b32 m; neg.f16x2 m, %2; fma.rn.f16x2 %0, %1, %3, m; }"
+      : "=r"(n.high[1]) : "r"(odd), "r"(n.low[1]), "r"(0x74007400u));
+  return n;
+}
+template <bool first>
+__device__ __forceinline__ void mma_word(float (&c)[4], float (&h)[4], uint32_t w, uint32_t u, uint32_t l0, uint32_t l1,
+                                         uint32_t h0, uint32_t h1) {
+  const Nibbles a = nibbles(w), b = nibbles(u);
+  if (first) {
+    mma16816_zero(c, a.low[0], b.low[0], a.low[1], b.low[1], l0, l1);
+    mma16816_zero(h, a.high[0], b.high[0], a.high[1], b.high[1], h0, h1);
+  } else {
+    mma16816(c, a.low[0], b.low[0], a.low[1], b.low[1], l0, l1);
+    mma16816(h, a.high[0], b.high[0], a.high[1], b.high[1], h0, h1);
+  }
+}
 __device__ __forceinline__ float half_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -124,7 +156,7 @@ __device__ __forceinline__ void put_x(float4 v, float mx, float sum, int vec, in
     if (RT == ROW_Q4_K) {  // lane t: 16 bytes, half t % 2 of a run of 64; nibble: which sub-block of it
       t = (b >> 1 & 1) * 2 + r / 16;
       nib = b & 1;
-    } else if (RT == ROW_Q4_0) {  // every second block: 36 bytes apart, the quad's lanes meet four banks
+    } else if (is_q4_0(RT)) {  // every second block: 36 bytes apart, the quad's lanes meet four banks
       quad = b / 8 * 2 + b % 2;
       t = b / 2 & 3;
     }
@@ -186,8 +218,14 @@ __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t
       }
     }
 #pragma unroll
-    for (int n = 0; n < AHEAD; ++n)
+    for (int n = 0; n < AHEAD; ++n) {
+      if (RT == ROW_Q4_0_PAIRS) {  // an even block's bytes are used from the third on, its first two last
+        const int next = (threadIdx.x & 28) | ((threadIdx.x + 1) & 3);
+        const float a = __shfl_sync(0xffffffffu, v[n].x, next), b = __shfl_sync(0xffffffffu, v[n].y, next);
+        if (va[n] % 64 < 32) v[n] = make_float4(v[n].z, v[n].w, a, b);
+      }
       if (vv[n] < nv) put_x<RT, C>(v[n], mx[n], sum[n], vv[n], va[n], xf, info);
+    }
   }
 }
 
@@ -207,6 +245,9 @@ __device__ __forceinline__ void q4k_scale(uint4 h, int j, float& d, float& m) {
   m = -half_bits(h.x >> 16) * (float)mn;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -223,20 +264,21 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
   uint8_t* xf = sm + WARPS * DEPTH * STAGE;
   float2* info = reinterpret_cast<float2*>(xf + (size_t)(p.nu * 256) * C::XBYTES);
   float* red = reinterpret_cast<float*>(info + p.nu * 8 * C::VECS);  // [2][warps][16 * VECS]
-  float4* zero = reinterpret_cast<float4*>(red + 2 * WARPS * 16 * C::VECS);
+  float4* zero = reinterpret_cast<float4*>(red + 2 * WARPS * 16 * C::JOIN);
   const int groups = WARPS / p.ks, group = warp / p.ks, part = warp % p.ks;
   const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
   const int ua = p.nu * part / p.ks, ub = p.nu * (part + 1) / p.ks, per_tile = ub - ua;
   const int my_tiles = first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
   const int steps = my_tiles * per_tile;
   // bytes of a row's full run
-  constexpr int RUN = RT == ROW_Q4_0 ? 144 : RT == ROW_Q4_1 ? 160 : RT == ROW_Q4_K ? 144 : 128;
+  constexpr int RUN = is_q4_0(RT) ? 144 : RT == ROW_Q4_1 ? 160 : RT == ROW_Q4_K ? 144 : 128;
   constexpr int BLOCK = RUN / 8;
 
   if (p.pdl) pdl_launch_dependents();
   // ---- weights: the copies of one step -----------------------------------------------
   // The 16 rows' windows in 16-byte pieces, consecutive pieces on consecutive lanes: an
-  // instruction then touches few lines. Tiles and full runs start at multiples of 16 bytes,
+  // instruction then touches few lines (four lanes a row, eight rows at once, are fewer
+  // instructions and slower: 33.6 -> 36.9 us for the 128,000 x 2048 head). Tiles and full runs start at multiples of 16 bytes,
   // so where a lane's pieces are within them never changes.
   constexpr int PIECES = RT == ROW_Q4_K || RT == ROW_PLANES ? RUN / 16 : RUN / 16 + 1;
   constexpr int TURNS = (16 * PIECES + 31) / 32;
@@ -257,7 +299,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
       if (c_tile + 1 < p.tiles && c_u * 8 + 8 <= p.nb) {
 #pragma unroll
         for (int i = 0; i < TURNS; ++i)
-          if (from[i] >= 0) copy16(c_at + to[i], c_src + from[i], 16);
+          if (from[i] >= 0) copy16(c_at + to[i], c_src + from[i]);
       } else {  // fewer rows, a partial run, and a last row that may end inside a piece
         const int rows = min(16, p.a.rows - c_tile * 16), bytes = min(8, p.nb - c_u * 8) * BLOCK;
 #pragma unroll
@@ -338,24 +380,34 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
   float2 xin[2];
   int stage = 0;
   const bool add = (p.a.flags & MOE_ACCUMULATE) != 0;
+  auto get = [&](int64_t at) {
+    return p.a.y_type == MOE_F32   ? static_cast<const float*>(p.a.y)[at]
+           : p.a.y_type == MOE_F16 ? __half2float(static_cast<const __half*>(p.a.y)[at])
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.a.y)[at]);
+  };
+  auto put = [&](int64_t at, float v) {
+    if (p.a.y_type == MOE_F32) static_cast<float*>(p.a.y)[at] = v;
+    else if (p.a.y_type == MOE_F16) static_cast<__half*>(p.a.y)[at] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p.a.y)[at] = __float2bfloat16_rn(v);
+  };
+  float old = 0.f, first_sums[2] = {0.f, 0.f};
   for (int k = 0, tile = first; k < my_tiles; ++k, tile += stride) {
-    // what a single vector's sums will be added to, loaded while they are made
-    float old = 0.f;
-    if (!C::MULTI && part * 32 + lane < 16 && tile * 16 + lane < p.a.rows) {
-      const int64_t row = (int64_t)tile * 16 + lane, at = t0 * p.a.ys + row;
-      if (add)
-        old = p.a.y_type == MOE_F32   ? static_cast<const float*>(p.a.y)[at]
-              : p.a.y_type == MOE_F16 ? __half2float(static_cast<const __half*>(p.a.y)[at])
-                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.a.y)[at]);
-      if (p.a.bias) old += p.a.bias[row];
+    // single vector: the pair's join is this warp's; what its sums will be added to is loaded while
+    // they are made
+    const bool join = !C::MULTI && (k >> 1 & (p.ks - 1)) == part;
+    const int64_t my_row = ((int64_t)(k & 1 ? tile - stride : tile) + (lane >> 4) * stride) * 16 + (lane & 15);
+    if (join && !(k & 1)) {
+      old = 0.f;
+      if (add && my_row < p.a.rows) old = get(t0 * p.a.ys + my_row);
+      if (p.a.bias && my_row < p.a.rows) old += p.a.bias[my_row];
     }
     for (int u0 = ua; u0 < ub; ++u0) {
       if constexpr (!C::MULTI) {
         if (k == 0 || per_tile > 1) {
 #pragma unroll
           for (int qq = 0; qq < 2; ++qq) {
-            xin[qq] = info[u0 * 8 + (RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t)];
-            if (RT == ROW_Q4_0) xin[qq].y *= -8.f;
+            xin[qq] = info[u0 * 8 + (is_q4_0(RT) ? 2 * t + qq : qq * 4 + t)];
+            if (is_q4_0(RT)) xin[qq].y *= -8.f;
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -382,7 +434,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
           const uint32_t h = *reinterpret_cast<const uint32_t*>(base[r] + b * 20);
           d = half_bits(h & 0xffffu);
           m = half_bits(h >> 16);
-        } else if constexpr (RT == ROW_Q4_0) {
+        } else if constexpr (is_q4_0(RT)) {
           d = half_bits(*reinterpret_cast<const uint16_t*>(base[r] + b * 18));
           m = -8.f * d;
         } else if constexpr (RT == ROW_Q4_K) {
@@ -396,12 +448,24 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
 #pragma unroll
       for (int qq = 0; qq < 2; ++qq) {
         if constexpr (!C::MULTI) {
-          const int b = RT == ROW_Q4_0 ? 2 * t + qq : qq * 4 + t;  // this lane's block of the run
+          const int b = is_q4_0(RT) ? 2 * t + qq : qq * 4 + t;  // this lane's block of the run
           float dd[2], mm[2];
           uint32_t w[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            if constexpr (RT == ROW_Q4_0) {
+            if constexpr (RT == ROW_Q4_0_PAIRS) {
+              const uint32_t* u = reinterpret_cast<const uint32_t*>(base[r] + t * 36);
+              if (qq == 0) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) w[r][i] = u[i + 1];
+                w[r][3] = __byte_perm(u[4], u[0], 0x7610);
+                dd[r] = half_bits(u[0] & 0xffffu);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[r][i] = u[i + 5];
+                dd[r] = half_bits(u[4] >> 16);
+              }
+            } else if constexpr (RT == ROW_Q4_0) {
               const uint32_t* u = reinterpret_cast<const uint32_t*>(st + word_at[r][qq]);
               uint32_t v[5];
 #pragma unroll
@@ -424,22 +488,19 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
               scale_of(r, b, dd[r], mm[r]);
             }
           }
-          float c[4];
-          mma_low<true>(c, w[0][0], w[1][0], x[qq][0].x, x[qq][0].y);
-          mma_high<false>(c, w[0][0], w[1][0], x[qq][2].x, x[qq][2].y);
-          mma_low<false>(c, w[0][1], w[1][1], x[qq][0].z, x[qq][0].w);
-          mma_high<false>(c, w[0][1], w[1][1], x[qq][2].z, x[qq][2].w);
-          mma_low<false>(c, w[0][2], w[1][2], x[qq][1].x, x[qq][1].y);
-          mma_high<false>(c, w[0][2], w[1][2], x[qq][3].x, x[qq][3].y);
-          mma_low<false>(c, w[0][3], w[1][3], x[qq][1].z, x[qq][1].w);
-          mma_high<false>(c, w[0][3], w[1][3], x[qq][3].z, x[qq][3].w);
+          float c[4], h[4];
+          mma_word<true>(c, h, w[0][0], w[1][0], x[qq][0].x, x[qq][0].y, x[qq][2].x, x[qq][2].y);
+          mma_word<false>(c, h, w[0][1], w[1][1], x[qq][0].z, x[qq][0].w, x[qq][2].z, x[qq][2].w);
+          mma_word<false>(c, h, w[0][2], w[1][2], x[qq][1].x, x[qq][1].y, x[qq][3].x, x[qq][3].y);
+          mma_word<false>(c, h, w[0][3], w[1][3], x[qq][1].z, x[qq][1].w, x[qq][3].z, x[qq][3].w);
           if (u0 * 8 + b < p.nb) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              if (RT == ROW_Q4_0) {  // d (sum q x - 8 sum x)
-                acc[0][0][r] = fmaf(dd[r], fmaf(xin[qq].x, c[2 * r] + c[2 * r + 1], xin[qq].y), acc[0][0][r]);
+              const float s = fmaf(h[2 * r] + h[2 * r + 1], 0.0625f, c[2 * r] + c[2 * r + 1]);
+              if (is_q4_0(RT)) {  // d (sum q x - 8 sum x)
+                acc[0][0][r] = fmaf(dd[r], fmaf(xin[qq].x, s, xin[qq].y), acc[0][0][r]);
               } else {
-                acc[0][0][r] = fmaf(dd[r] * xin[qq].x, c[2 * r] + c[2 * r + 1], acc[0][0][r]);
+                acc[0][0][r] = fmaf(dd[r] * xin[qq].x, s, acc[0][0][r]);
                 acc[0][0][r] = fmaf(mm[r], xin[qq].y, acc[0][0][r]);
               }
             }
@@ -500,42 +561,49 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
       __syncwarp();
       copy_step();
     }
-    // ---- join the partial sums of the tile, in order ------------------------------------
-    float* mine = red + ((k & 1) * WARPS + warp) * 16 * C::VECS;
+    // ---- join the partial sums, in order --------------------------------------------------
+    if constexpr (!C::MULTI) {  // of two tiles at once
+      if (!(k & 1) && k + 1 < my_tiles) {
+        first_sums[0] = acc[0][0][0];
+        first_sums[1] = acc[0][0][1];
+        acc[0][0][0] = acc[0][0][1] = 0.f;
+        continue;
+      }
+      // four sums a lane, each over the quad's lanes: lane t keeps sum t (row g + 8 (t & 1) of tile t / 2)
+      float v[4] = {k & 1 ? first_sums[0] : acc[0][0][0], k & 1 ? first_sums[1] : acc[0][0][1], acc[0][0][0], acc[0][0][1]};
+      acc[0][0][0] = acc[0][0][1] = 0.f;
+      const float a = (t & 2 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, t & 2 ? v[0] : v[2], 2);
+      const float b = (t & 2 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, t & 2 ? v[1] : v[3], 2);
+      const float s = (t & 1 ? b : a) + __shfl_xor_sync(0xffffffffu, t & 1 ? a : b, 1);
+      float* sums = red + ((k >> 1 & 1) * WARPS + group * p.ks) * 32;
+      sums[part * 32 + (t >> 1) * 16 + (t & 1) * 8 + g] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.ks * 32) : "memory");
+      if (join && my_row < p.a.rows) {
+        float sum = 0.f;
+        for (int w = 0; w < p.ks; ++w) sum += sums[w * 32 + lane];
+        put(t0 * p.a.ys + my_row, sum + old);
+      }
+    } else {
+      float* mine = red + ((k & 1) * WARPS + warp) * 16 * C::VECS;
 #pragma unroll
-    for (int n = 0; n < C::NT; ++n)
+      for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-      for (int v = 0; v < AV; ++v)
+        for (int v = 0; v < AV; ++v)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float s = acc[n][v][r];
-          acc[n][v][r] = 0.f;
-          if constexpr (!C::MULTI) {
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if (t == 0) mine[g + 8 * r] = s;
-          } else {
-            mine[((n * 4 + t) * AV + v) * 16 + g + 8 * r] = s;
+          for (int r = 0; r < 2; ++r) {
+            mine[((n * 4 + t) * AV + v) * 16 + g + 8 * r] = acc[n][v][r];
+            acc[n][v][r] = 0.f;
           }
-        }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.ks * 32) : "memory");
-    for (int i = part * 32 + lane; i < 16 * nv; i += p.ks * 32) {
-      const int64_t row = (int64_t)tile * 16 + i % 16;
-      if (row >= p.a.rows) continue;
-      const float* from = red + ((k & 1) * WARPS + group * p.ks) * 16 * C::VECS + i;
-      float s = 0.f;
-      for (int w = 0; w < p.ks; ++w) s += from[w * 16 * C::VECS];
-      const int64_t at = (t0 + i / 16) * p.a.ys + row;
-      if (C::MULTI && p.a.bias) s += p.a.bias[row];
-      if (p.a.y_type == MOE_F32) {
-        float* y = static_cast<float*>(p.a.y) + at;
-        *y = s + (!C::MULTI ? old : add ? *y : 0.f);
-      } else if (p.a.y_type == MOE_F16) {
-        __half* y = static_cast<__half*>(p.a.y) + at;
-        *y = __float2half_rn(s + (!C::MULTI ? old : add ? __half2float(*y) : 0.f));
-      } else {
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.a.y) + at;
-        *y = __float2bfloat16_rn(s + (!C::MULTI ? old : add ? __bfloat162float(*y) : 0.f));
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(p.ks * 32) : "memory");
+      for (int i = part * 32 + lane; i < 16 * nv; i += p.ks * 32) {
+        const int64_t row = (int64_t)tile * 16 + i % 16;
+        if (row >= p.a.rows) continue;
+        const float* from = red + ((k & 1) * WARPS + group * p.ks) * 16 * C::VECS + i;
+        float s = 0.f;
+        for (int w = 0; w < p.ks; ++w) s += from[w * 16 * C::VECS];
+        if (p.a.bias) s += p.a.bias[row];
+        const int64_t at = (t0 + i / 16) * p.a.ys + row;
+        put(at, s + (add ? get(at) : 0.f));
       }
     }
   }
@@ -549,7 +617,7 @@ template <int RT, class C>
 int smem_bytes(const MvArgs& p) {
   const int stage = 16 * (MV_PITCH + (RT == ROW_PLANES ? 2 * MV_SPITCH : 0));
   return C::WARPS * C::DEPTH * stage + p.nu * 256 * C::XBYTES + p.nu * 8 * C::VECS * 8 +
-         2 * C::WARPS * 16 * C::VECS * 4 + 16;
+         2 * C::WARPS * 16 * C::JOIN * 4 + 16;
 }
 
 template <int RT, class C>
@@ -612,6 +680,8 @@ cudaError_t launch_cols(MvArgs& p, cudaStream_t st) {
       return e;
     if (try_launch<RT, Cols<true, 1, 2, 16>>(p, st, &e) || try_launch<RT, Cols<true, 1, 2, 8>>(p, st, &e)) return e;
   }
+  if constexpr (RT == ROW_Q4_0)
+    if (p.nb % 2 == 0) return launch<ROW_Q4_0_PAIRS, Cols<false, 1, 2, 8>>(p, st);
   return launch<RT, Cols<false, 1, 2, 8>>(p, st);
 }
 
