@@ -77,18 +77,19 @@ __global__ void __launch_bounds__(256) lin_step(LinattnArgs a) {
   }
 }
 
-constexpr int SCAN_TOK = 16;  // tokens staged at a time
-
-// A warp holds the state's columns for 8 values of v; lane = 8 * part + column, and the part
-// owns the key values 16 j + 4 part + (0 .. 3), so o_t is two shuffles away from its sum.
-// A CTA of 4 warps takes 32 columns of one head of one sequence. DKP: key_dim rounded up to
-// 64 or 128. The next tokens are on their way while these are walked.
-template <typename T, int DKP>
-__global__ void __launch_bounds__(128) lin_scan(LinattnArgs a) {
-  __shared__ __align__(16) float qs[SCAN_TOK][DKP], ks[SCAN_TOK][DKP], vs[SCAN_TOK][32], ls[SCAN_TOK];
-  const int tid = threadIdx.x, lane = tid & 31;
+// A warp holds 8 columns of the state, or a quarter of their rows (KQ 4); lane = 8 * part +
+// column, and the part owns the key values 16 j + 4 part + (0 .. 3) of the warp's, so a warp's
+// share of o_t is two shuffles away. A CTA takes 32 columns of one head of one sequence in four
+// warps, or 16 in eight, whose shares are joined when the staged tokens have been walked. DKP:
+// key_dim rounded up to 64 or 128. The next tokens are on their way while these are walked.
+template <typename T, int DKP, int KQ>
+__global__ void __launch_bounds__(KQ == 1 ? 128 : 256) lin_scan(LinattnArgs a) {
+  constexpr int COLS = KQ == 1 ? 32 : 16, NT = COLS * 4 * KQ, TOK = KQ == 1 ? 16 : 32;  // TOK: tokens staged at a time
+  __shared__ __align__(16) float qs[TOK][DKP], ks[TOK][DKP], vs[TOK][COLS], ls[TOK];
+  __shared__ float shares[KQ == 1 ? 1 : TOK][KQ][COLS];
+  const int tid = threadIdx.x, lane = tid & 31, kq = tid / 32 % KQ;
   const int h = blockIdx.y, b = blockIdx.z;
-  const int col0 = blockIdx.x * 32, lc = (tid >> 5) * 8 + (lane & 7), col = col0 + lc, part = lane >> 3;
+  const int col0 = blockIdx.x * COLS, lc = tid / (32 * KQ) * 8 + (lane & 7), col = col0 + lc, part = lane >> 3;
   pdl_wait_prior_grids();
   const bool live = col < a.dv;
   int begin, end;
@@ -96,56 +97,59 @@ __global__ void __launch_bounds__(128) lin_scan(LinattnArgs a) {
   const int slot = seq_slot(a, b);
   T* o = static_cast<T*>(a.o) + (int64_t)h * a.dv;
   if (slot < 0) {
-    for (int t = begin + part; t < end; t += 4)
+    for (int t = begin + kq * 4 + part; t < end; t += 4 * KQ)
       if (live) o[t * a.os + col] = from_f32<T>(0.f);
     return;
   }
   const T* q = static_cast<const T*>(a.q) + (int64_t)(h / a.rep) * a.dk;
   const T* k = static_cast<const T*>(a.k) + (int64_t)(h / a.rep) * a.dk;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
-  constexpr int QN = SCAN_TOK * DKP / 4 / 128;  // four-value pieces of a thread
+  constexpr int QN = TOK * DKP / 4 / NT;  // four-value pieces of a thread
   float4 nq[QN], nk[QN], nv;
   float ng = 0.f;
   auto fetch = [&](int t0) {
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
-      const int at = i * 128 + tid, t = t0 + at / (DKP / 4), d = at % (DKP / 4) * 4;
+      const int at = i * NT + tid, t = t0 + at / (DKP / 4), d = at % (DKP / 4) * 4;
       const bool in = t < end && d < a.dk;
       nq[i] = in ? load4(q + t * a.qs + d) : z;
       nk[i] = in ? load4(k + t * a.ks + d) : z;
     }
-    const int t = t0 + tid / 8, d = col0 + tid % 8 * 4;
-    nv = t < end && d < a.dv ? load4(v + t * a.vs + d) : z;
-    if (tid < SCAN_TOK && t0 + tid < end) ng = a.g[a.token_decay ? (int64_t)(t0 + tid) * a.H + h : h];
+    const int t = t0 + tid / (COLS / 4), d = col0 + tid % (COLS / 4) * 4;
+    nv = tid < TOK * COLS / 4 && t < end && d < a.dv ? load4(v + t * a.vs + d) : z;
+    if (tid < TOK && t0 + tid < end) ng = a.g[a.token_decay ? (int64_t)(t0 + tid) * a.H + h : h];
   };
   fetch(begin);
   float* st = a.state + ((int64_t)slot * a.H + h) * a.dk * a.dv;
-  float S[DKP / 4];
+  constexpr int ROWS = DKP / 4 / KQ;
+  float S[ROWS];
 #pragma unroll
-  for (int i = 0; i < DKP / 4; ++i) {
-    const int d = i / 4 * 16 + part * 4 + i % 4;
+  for (int i = 0; i < ROWS; ++i) {
+    const int d = kq * (DKP / KQ) + i / 4 * 16 + part * 4 + i % 4;
     S[i] = live && d < a.dk && !a.fresh ? st[d * a.dv + col] : 0.f;
   }
-  for (int t0 = begin; t0 < end; t0 += SCAN_TOK) {
-    const int n = min(SCAN_TOK, end - t0);
+  for (int t0 = begin; t0 < end; t0 += TOK) {
+    const int n = min(TOK, end - t0);
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
-      const int at = i * 128 + tid;
+      const int at = i * NT + tid;
       *reinterpret_cast<float4*>(&qs[at / (DKP / 4)][at % (DKP / 4) * 4]) = nq[i];
       *reinterpret_cast<float4*>(&ks[at / (DKP / 4)][at % (DKP / 4) * 4]) = nk[i];
     }
-    *reinterpret_cast<float4*>(&vs[tid / 8][tid % 8 * 4]) = nv;
+    if (tid < TOK * COLS / 4) *reinterpret_cast<float4*>(&vs[tid / (COLS / 4)][tid % (COLS / 4) * 4]) = nv;
     if (tid < n) ls[tid] = expf(ng);
     __syncthreads();
-    if (t0 + SCAN_TOK < end) fetch(t0 + SCAN_TOK);
+    if (t0 + TOK < end) fetch(t0 + TOK);
+#pragma unroll 4
     for (int t = 0; t < n; ++t) {
       const float lam = ls[t], vv = vs[t][lc];
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < DKP / 16; ++i) {
-        const float4 kk = *reinterpret_cast<const float4*>(&ks[t][i * 16 + part * 4]);
-        const float4 qq = *reinterpret_cast<const float4*>(&qs[t][i * 16 + part * 4]);
+      for (int i = 0; i < ROWS / 4; ++i) {
+        const int d = kq * (DKP / KQ) + i * 16 + part * 4;
+        const float4 kk = *reinterpret_cast<const float4*>(&ks[t][d]);
+        const float4 qq = *reinterpret_cast<const float4*>(&qs[t][d]);
         const float k4[4] = {kk.x, kk.y, kk.z, kk.w}, q4[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -156,13 +160,27 @@ __global__ void __launch_bounds__(128) lin_scan(LinattnArgs a) {
       float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (live && part == 0) o[(t0 + t) * a.os + col] = from_f32<T>(s * a.scale);
+      if (KQ > 1) {
+        if (part == 0) shares[t][kq][lc] = s;
+      } else if (live && part == 0) {
+        o[(t0 + t) * a.os + col] = from_f32<T>(s * a.scale);
+      }
     }
     __syncthreads();
+    if (KQ > 1) {
+      for (int i = tid; i < n * COLS; i += NT) {
+        const int t = i / COLS, c = i % COLS;
+        if (col0 + c >= a.dv) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < KQ; ++w) s += shares[t][w][c];
+        o[(t0 + t) * a.os + col0 + c] = from_f32<T>(s * a.scale);
+      }
+    }
   }
 #pragma unroll
-  for (int i = 0; i < DKP / 4; ++i) {
-    const int d = i / 4 * 16 + part * 4 + i % 4;
+  for (int i = 0; i < ROWS; ++i) {
+    const int d = kq * (DKP / KQ) + i / 4 * 16 + part * 4 + i % 4;
     if (live && d < a.dk) st[d * a.dv + col] = S[i];
   }
 }
@@ -181,10 +199,12 @@ cudaError_t launch(K kern, dim3 grid, int threads, bool pdl, cudaStream_t st, co
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T>
+template <typename T, int KQ>
 cudaError_t scan_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.dv + 31) / 32), (unsigned)a.H, (unsigned)a.B);
-  return a.dk <= 64 ? launch(lin_scan<T, 64>, grid, 128, pdl, st, a) : launch(lin_scan<T, 128>, grid, 128, pdl, st, a);
+  constexpr int COLS = KQ == 1 ? 32 : 16;
+  const dim3 grid((unsigned)((a.dv + COLS - 1) / COLS), (unsigned)a.H, (unsigned)a.B);
+  return a.dk <= 64 ? launch(lin_scan<T, 64, KQ>, grid, COLS * 4 * KQ, pdl, st, a)
+                    : launch(lin_scan<T, 128, KQ>, grid, COLS * 4 * KQ, pdl, st, a);
 }
 
 template <typename T>
@@ -197,17 +217,46 @@ cudaError_t step_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
   return launch(lin_step<T, 8>, dim3((unsigned)((a.dv + 31) / 32), (unsigned)a.H, (unsigned)a.B), 256, pdl, st, a);
 }
 
+// Whether a walk takes CTAs of 16 columns: if they are one an SM at most (64 tokens: 16 heads 9.0 us,
+// 12.8 with 32 columns; 32 heads 12.4 and 12.9; 64 heads 23.4 and 17.8).
+bool scan_few(const LinattnArgs& a) { return (int64_t)a.B * a.H * ((a.dv + 15) / 16) <= 152; }
+
+// Whether walking the tokens is quicker than chunks, by what each takes in ns at widths of 128
+// (heads: of all sequences). The walk: launch, the states both ways, each token of the longest
+// sequence and, where heads fill the SMs, each token of each head. Chunks: a chain of them for
+// a sequence, or waves of heads. Measured, us, walk / bf16 chunks (f32 chunks):
+//   tokens x heads    32 x 16: 5.2 / 10.1 (13.6)   64 x 16: 9.0 / 9.8 (15.7)   128 x 16: 16.2 / 13.0 (24.3)
+//                     32 x 64: 10.2 / 10.7   32 x 256: 28 / 14.5 (28.5)   4 x 2048: 70 / 92   16 x 2048: 124 / 95
+// With offsets only the total is known here: one sequence may have all of it. Beyond 256 tokens
+// chunks are cut into units that run side by side.
+bool scan_is_quicker(const LinattnArgs& a, int type, bool few) {
+  const double heads = (double)a.B * a.H, longest = a.offsets ? a.N : a.seq_len, work = (double)a.N * a.H;
+  if (longest > 256) return false;
+  const double cols = ((a.dv + 31) / 32) / 4.0, chunks = ((int)longest + 63) / 64;
+  const double crowd = work - 32 * longest;
+  const double scan = 2300 + 20 * heads * cols + (few ? 108 : 165) * longest + (crowd > 0 ? 2.6 * crowd * cols : 0);
+  double chain, wave;
+  if (type == MOE_F32) {
+    chain = 7500 + 8300 * chunks;
+    wave = heads * (52 + 63 * chunks);
+  } else if (type == MOE_F16) {
+    chain = 7000 + 4000 * chunks;
+    wave = heads * (38 + 17 * chunks);
+  } else {
+    chain = 7000 + 3000 * chunks;
+    wave = heads * (36 + 14 * chunks);
+  }
+  return scan < (chain > wave ? chain : wave);
+}
+
 }  // namespace
 
 cudaError_t linattn_prefill_launch(const LinattnArgs& a, int type, void* ws, bool pdl, cudaStream_t st) {
-  // Prompts that are walked token by token: as long as that is quicker than one chunk (one
-  // sequence, 16 heads of 128: the walk takes 2.3 us and 0.2 us a token, a chunk 8.9 us in bf16,
-  // 11 in f16, 16 in f32). With offsets only the total is known here.
-  const int most = type == MOE_F32 ? 64 : 36;
-  if ((a.offsets ? a.N : a.seq_len) > most) return linattn_chunk_launch(a, type, ws, pdl, st);
-  if (type == MOE_F32) return scan_launch<float>(a, pdl, st);
-  if (type == MOE_F16) return scan_launch<__half>(a, pdl, st);
-  return scan_launch<__nv_bfloat16>(a, pdl, st);
+  const bool few = scan_few(a);
+  if (!scan_is_quicker(a, type, few)) return linattn_chunk_launch(a, type, ws, pdl, st);
+  if (type == MOE_F32) return few ? scan_launch<float, 4>(a, pdl, st) : scan_launch<float, 1>(a, pdl, st);
+  if (type == MOE_F16) return few ? scan_launch<__half, 4>(a, pdl, st) : scan_launch<__half, 1>(a, pdl, st);
+  return few ? scan_launch<__nv_bfloat16, 4>(a, pdl, st) : scan_launch<__nv_bfloat16, 1>(a, pdl, st);
 }
 
 cudaError_t linattn_step_launch(const LinattnArgs& a, int type, bool pdl, cudaStream_t st) {
