@@ -191,7 +191,7 @@ int moe_q4_matvec(const void* x, const void* weights, const void* scales, const 
 size_t moe_linattn_workspace_size(const moe_linattn_cfg* c) {
   moe::clear_error();
   if (check_linattn(c) != MOE_OK) return 0;
-  return moe::linattn_split(c->n_tokens, c->n_seq, c->n_heads, c->key_dim, c->value_dim, c->type).total;
+  return moe::linattn_workspace(c->n_tokens, c->n_heads, c->key_dim, c->value_dim, c->type);
 }
 
 int moe_linattn_prefill(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* offsets,

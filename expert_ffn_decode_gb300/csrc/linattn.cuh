@@ -29,20 +29,38 @@ __host__ __device__ __forceinline__ int seq_units(int n, int seg) { return n > s
 struct Unit {
   int b;      // sequence
   int i, n;   // unit i of n
+  int seg;    // tokens of a unit
   int slot0;  // workspace state of the sequence's unit 0 (sequences of several units)
   bool found;
 };
 constexpr int UNIT_SCRATCH = 4 + 3 * 8;  // ints of shared memory that find_unit takes (8 warps)
 // Unit u of the call: u < B are the last (or only) units of the sequences, u >= B counts the
 // others, each of seg tokens, in sequence order. Of up to 256 sequences the last units of more
-// than half of seg come first, so that a grid in this order ends with its shortest pieces. A
-// whole CTA (256 threads of it) adds up what the sequences before it have. `n_ws`: states in the
-// workspace; a sequence whose units would not fit (offsets that descend can make sequences
-// share tokens) is not found.
-__device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_ws, int u, int* scratch) {
+// than half of seg come first (`by_rank`), so that a grid in this order ends with its shortest
+// pieces. A whole CTA (256 threads of it) settles whether the call stays whole, where that is
+// open, and adds up what the sequences before u's have. `n_ws`: states in the workspace; a
+// sequence whose units would not fit (offsets that descend can make sequences share tokens) is
+// not found.
+__device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, int n_ws, int u, int* scratch,
+                                          bool by_rank = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool ranked = a.B <= 256;
-  Unit r{0, 0, 1, 0, true};
+  const bool ranked = by_rank && a.B <= 256;
+  int first = 0, past = 0, seg = cut.seg;  // of sequence tid
+  if (tid < min(256, a.B)) seq_range(a, tid, first, past);
+  if (cut.ask) {
+    int longest = past - first;
+    for (int b = 256 + tid; tid < 256 && b < a.B; b += 256) {
+      int begin, end;
+      seq_range(a, b, begin, end);
+      longest = max(longest, end - begin);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0 && warp < 8) scratch[4 + warp] = longest;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) longest = max(longest, scratch[4 + w]);
+    if (longest <= cut.whole) seg = cut.whole;
+  }
+  Unit r{0, 0, 1, seg, 0, true};
   if (u < a.B && (a.B == 1 || !ranked)) {
     int begin, end;
     seq_range(a, u, begin, end);
@@ -57,8 +75,8 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, int seg, int n_w
     const int b = tid < 256 ? b0 + tid : a.B;
     int ns = 0, tail = 0;
     if (b < a.B) {
-      int begin, end;
-      seq_range(a, b, begin, end);
+      int begin = first, end = past;
+      if (b0 > 0) seq_range(a, b, begin, end);
       ns = seq_units(end - begin, seg);
       tail = end - begin - (ns - 1) * seg;
     }

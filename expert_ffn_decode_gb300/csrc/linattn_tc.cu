@@ -368,7 +368,7 @@ struct Maps {
 
 // MODE 0: the state that a unit's tokens alone leave, and its decay, into the workspace.
 // MODE 1: the outputs, from the state before the unit; the sequence's last unit stores it.
-// `wd`: decays [states][H], `wst`: states [states][H][dk][dv]; seg: tokens of a unit. WIDE: keys
+// `wd`: decays [states][H], `wst`: states [states][H][dk][dv]. WIDE: keys
 // of more than 112 values, whose eight steps along K are then fixed (237 against 259 us for
 // 16,384 tokens x 32 heads of 128).
 //
@@ -381,7 +381,7 @@ struct Maps {
 // f32 has one of sixteen warps, and its products of a chunk start when its tiles are written.
 template <typename T, int NP, int MODE, bool WIDE>
 __global__ void __launch_bounds__(chunk_threads(NP), NP == 1 ? 2 : 1)
-lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, int behind_join, float* wd, float* wst,
+lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int n_ws, int behind_join, float* wd, float* wst,
           uint32_t* ctrl) {
   using L = Plan<NP>;
   static_assert(sizeof(Misc<chunk_threads(NP) / 128>) <= L::BYTES - L::MISC, "misc");
@@ -406,7 +406,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, i
   // Behind the join everything but the states is older than the state pass, which has ended: this
   // grid then sets up and loads its first chunk beside the join and waits for the states alone.
   if (!behind_join) pdl_wait_prior_grids();
-  const Unit un = find_unit(a, seg, n_ws, u, m->scratch);
+  const Unit un = find_unit(a, cut, n_ws, u, m->scratch);
   if (!un.found) {
     if (behind_join) pdl_wait_prior_grids();  // no grid ends before the one it stands behind
     return;
@@ -414,8 +414,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, i
   int begin, end;
   seq_range(a, un.b, begin, end);
   const int last = end;
-  begin += un.i * seg;
-  end = min(begin + seg, end);
+  begin += un.i * un.seg;
+  end = min(begin + un.seg, end);
   const int slot = seq_slot(a, un.b);
   T* o = static_cast<T*>(a.o) + (int64_t)h * a.dv;
   if (slot < 0) {
@@ -905,12 +905,17 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, int seg, int n_ws, i
 // each next one adds what the unit between leaves, in order. A thread keeps eight units of
 // 2 x 4 values in flight. `by_seq`: a CTA for each sequence, else for each unit, of which the
 // first does the work (many sequences, few of them long).
-__global__ void __launch_bounds__(256) lin_join(LinattnArgs a, int seg, int n_ws, int by_seq, const float* wd,
+__global__ void __launch_bounds__(256) lin_join(LinattnArgs a, LinattnCut cut, int n_ws, int by_seq, const float* wd,
                                                 float* wst) {
   __shared__ int scratch[UNIT_SCRATCH];
   pdl_wait_prior_grids();
   pdl_launch_dependents();  // the output pass may set up
-  const Unit un = find_unit(a, seg, n_ws, by_seq ? blockIdx.x : a.B + blockIdx.x, scratch);
+  if (by_seq) {  // most calls' sequences are whole
+    int begin, end;
+    seq_range(a, blockIdx.x, begin, end);
+    if (end - begin <= cut.seg) return;
+  }
+  const Unit un = find_unit(a, cut, n_ws, by_seq ? blockIdx.x : a.B + blockIdx.x, scratch, false);
   if (!un.found || un.n == 1 || (!by_seq && un.i != 0)) return;
   const int slot = seq_slot(a, un.b);
   if (slot < 0) return;
@@ -994,7 +999,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int t
 
 template <typename T, int NP, bool WIDE>
 cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, cudaStream_t st) {
-  const LinattnSplit sp = linattn_split(a.N, a.B, a.H, a.dk, a.dv, type);
+  const LinattnSplit sp = linattn_split(a.N, a.offsets ? a.N : a.seq_len, a.B, a.H, type);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws);
   float* wd = reinterpret_cast<float*>(ws + sp.decays);
   float* wst = reinterpret_cast<float*>(ws + sp.states);
@@ -1008,17 +1013,17 @@ cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, 
     if ((e = make_map(&maps.o, a.o, a.dv, a.H, a.N, a.os, false)) != cudaSuccess) return e;
   }
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
-  const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.seg * a.B;  // units but the last, at most
+  const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.cut.seg * a.B;  // units but the last, at most
   if (whole > 0) {
-    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws, 0, wd,
+    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws, 0, wd,
                wst, ctrl);
     if (e != cudaSuccess) return e;
     const int by_seq = a.B <= whole;
     const dim3 jgrid((unsigned)(by_seq ? a.B : whole), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
-    e = launch(lin_join, jgrid, 256, 0, pdl, st, a, sp.seg, sp.n_ws, by_seq, (const float*)wd, wst);
+    e = launch(lin_join, jgrid, 256, 0, pdl, st, a, sp.cut, sp.n_ws, by_seq, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.seg, sp.n_ws,
+  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws,
                 whole > 0 ? 1 : 0, wd, wst, ctrl);
 }
 

@@ -354,7 +354,8 @@ int moe_linattn_prefill(const void* q, const void* k, const void* v, const float
                         const int32_t* offsets, const int32_t* slots, const moe_linattn_cfg* cfg, float* state,
                         void* o, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of a moe_linattn_prefill call (0 for an invalid cfg). */
+/* Workspace bytes of a moe_linattn_prefill call (0 for an invalid cfg); fewer tokens of the
+ * same heads and type need no more. */
 size_t moe_linattn_workspace_size(const moe_linattn_cfg* cfg);
 
 /* One token for each sequence (row b of q, k, v, o and of a per-token log_decay is
