@@ -366,3 +366,24 @@ def test_states_past_32_bits():
     want = s.want()
     s.slots, s.n_states, s.state = c.slots, n, pool
     s.check(s.step(), pool[n - 1:], want)
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("offsets", [False, True])
+@pytest.mark.parametrize("lens,H", [([448] * 8, 10), ([512] * 3 + [1, 0, 512], 16), ([1500, 60, 0, 200], 30), ([33] * 5, 16),
+                                    ([200] * 4, 2)],
+                         ids=["equal", "some-empty", "one-long", "short", "few-heads"])
+def test_whole_or_cut(lens, H, offsets, type):
+    """Calls around the point where sequences are cut into units, and around the walk's."""
+    if not offsets and len(set(lens)) > 1:
+        lens = [max(lens)] * 3
+    c = Case(lens, H=H, dk=64, dv=40, type=type, decay="reset")
+    want = c.want()
+    c.check(c.prefill(**({} if offsets else {"offsets": None})), c.state, want)
+
+
+def test_many_sequences_with_one_length():
+    """More sequences than one round of the search takes, which the offsets leave whole."""
+    c = Case([130] * 300, H=1, dk=32, dv=32, type="bf16")
+    want = c.want()
+    c.check(c.prefill(), c.state, want)

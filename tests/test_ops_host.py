@@ -174,3 +174,12 @@ def test_oracle_linattn_closed_forms():
     o2, S2, _, _ = oo.linattn(q[5:], k[5:], v[5:], g[5:], 0 * S0, 0.5)
     np.testing.assert_allclose(o[5:], o2, rtol=1e-12)
     np.testing.assert_allclose(S, S2, rtol=1e-12)
+
+
+@pytest.mark.parametrize("type", [ffn.MOE_BF16, ffn.MOE_F32])
+@pytest.mark.parametrize("heads", [1, 4, 16, 37, 100, 304])
+def test_workspace_grows_with_the_tokens(built, heads, type):
+    """A workspace for the longest call serves the shorter ones, however many sequences they have."""
+    sizes = [ffn.moe_linattn_workspace_size(la_cfg(n_seq=b, n_tokens=n, n_heads=heads, n_qk_heads=1, n_states=9, type=type))
+             for n in range(1, 5000, 61) for b in (1, 7)]
+    assert all(0 < a <= b for a, b in zip(sizes, sizes[1:]))
