@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(256) lin_step(LinattnArgs a) {
 // column, and the part owns the key values 16 j + 4 part + (0 .. 3) of the warp's, so a warp's
 // share of o_t is two shuffles away. A CTA takes 32 columns of one head of one sequence in four
 // warps, or 16 in eight, whose shares are joined when the staged tokens have been walked. DKP:
-// key_dim rounded up to 64 or 128. The next tokens are on their way while these are walked.
+// key_dim rounded up to 64 or 128. What bounds a short prompt is each token's chain of shared
+// memory reads, products and shuffles: 16 heads take 2.5 us and 0.1 us a token. The next tokens
+// are on their way while these are walked.
 template <typename T, int DKP, int KQ>
 __global__ void __launch_bounds__(KQ == 1 ? 128 : 256) lin_scan(LinattnArgs a) {
   constexpr int COLS = KQ == 1 ? 32 : 16, NT = COLS * 4 * KQ, TOK = KQ == 1 ? 16 : 32;  // TOK: tokens staged at a time
@@ -209,7 +211,10 @@ cudaError_t scan_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
 
 template <typename T>
 cudaError_t step_launch(const LinattnArgs& a, bool pdl, cudaStream_t st) {
-  if ((int64_t)a.B * a.H >= 304) {  // as many CTAs as two an SM: a whole head each
+  // As many CTAs as two an SM: a whole head each (96 sequences x 32 heads 61.7 us, 63.0 in quarters);
+  // narrow heads in narrow CTAs (37 sequences x 10 heads of 72 x 40 3.0 us, 3.3 in parts of 32
+  // columns, 4.2 with 128).
+  if ((int64_t)a.B * a.H >= 304) {
     const dim3 grid(1, (unsigned)a.H, (unsigned)a.B);
     if (a.dv > 64) return launch(lin_step<T, 32>, grid, 256, pdl, st, a);
     if (a.dv > 32) return launch(lin_step<T, 16>, grid, 256, pdl, st, a);
