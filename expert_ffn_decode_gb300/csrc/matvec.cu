@@ -17,9 +17,12 @@
 // neighbours).
 //
 // x is held as f16 pieces: within a block of 32 values it is scaled by a power of two that
-// puts the largest magnitude at 2^13 .. 2^14, then split into two parts (22 bits of each value;
-// 16-bit types in calls of several vectors take one, which holds them). Sums are f32. (A 24-bit
-// fixed point of the block was 1.3 times outside the bound in the same place.)
+// puts the largest magnitude at 2^13 .. 2^14, then split into two parts (22 bits of each value
+// down to 2^-15 of the block's largest, fewer below; 16-bit types in calls of several vectors take
+// one, which holds them). A block's sums of q x and of x and their products with d and m stay in that
+// scale, in f32, and only then is the scale taken back: near f32's largest number a sum of x may
+// lie outside f32 where y does not. (A 24-bit fixed point of the block was 1.3 times outside
+// the bound in the same place.)
 //
 // Columns of one mma are (vector, part) pairs. A single vector has two of eight: the other six
 // take three more blocks. Lane t of a quad of lanes then holds a whole block's nibbles of its
@@ -133,17 +136,19 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// x in f16 pieces, and for each block and vector {2^10 / scale, sum of x}. A thread takes four
-// values of a vector; the eight threads of a block are neighbours. Values past the row's end
-// are not written: they belong to blocks whose sums are dropped.
+// The scale of a block of x, a power of two that brings its largest magnitude mx to 2^13 .. 2^14
+// (the smallest normal number comes to 2, and 0 stays), and 2^10 / scale; both normal.
+__device__ __forceinline__ float2 block_scale(float mx) {
+  const uint32_t e = min(max(__float_as_uint(mx) >> 23, 13u), 254u);
+  return make_float2(__uint_as_float((267 - e) << 23), __uint_as_float((e - 3) << 23));
+}
+// Scaled x in f16 pieces, and for each block and vector {2^10 / scale, 2^-10 sum of scaled x}. A thread
+// takes four values of a vector; the eight threads of a block are neighbours. Values past the row's
+// end are not written: they belong to blocks whose sums are dropped.
 template <int RT, class C>
-__device__ __forceinline__ void put_x(float4 v, float mx, float sum, int vec, int at, uint8_t* xf, float2* info) {
-  // largest magnitude 2^e (1 .. 2): scale 2^(13 - e); it and 2^10 / it stay normal
-  const int e = min(max((int)(__float_as_uint(mx) >> 23), 27), 253);
-  const float sc = __uint_as_float((uint32_t)(267 - e) << 23);
-  const float back = __uint_as_float((uint32_t)(e - 13) << 23);  // 1 / sc
+__device__ __forceinline__ void put_x(float4 v, float back, float sum, int vec, int at, uint8_t* xf, float2* info) {
   const int b = at / 32, r = at % 32;
-  const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
+  const float f[4] = {v.x, v.y, v.z, v.w};
   uint2 parts[2];
   parts[0] = make_uint2(pack_h2(f[0], f[2]), pack_h2(f[1], f[3]));
   if (C::PARTS == 2) {
@@ -171,7 +176,7 @@ __device__ __forceinline__ void put_x(float4 v, float mx, float sum, int vec, in
       *reinterpret_cast<uint2*>(xf + ((b * C::NT + col / 8) * 32 + lane) * 16 + r / 16 * 8) = parts[q];
     }
   }
-  if ((threadIdx.x & 7) == 0) info[b * C::VECS + vec] = make_float2(back * 1024.f, sum);
+  if ((threadIdx.x & 7) == 0) info[b * C::VECS + vec] = make_float2(back, sum * 0.0009765625f);
 }
 template <int RT, class C, typename TX>
 __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t* xf, float2* info) {
@@ -199,23 +204,31 @@ __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t
   for (int turn = 0; turn < turns; ++turn) {
     float4 v[AHEAD];
     int vv[AHEAD], va[AHEAD];
-    float mx[AHEAD], sum[AHEAD];
+    float mx[AHEAD], sum[AHEAD], back[AHEAD];
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
       v[n] = ld[n];
       vv[n] = lv[n];
       va[n] = la[n];
       mx[n] = fmaxf(fmaxf(fabsf(v[n].x), fabsf(v[n].y)), fmaxf(fabsf(v[n].z), fabsf(v[n].w)));
-      sum[n] = (v[n].x + v[n].y) + (v[n].z + v[n].w);
     }
     if (turn + 1 < turns) fetch();
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {  // over the 8 threads of a block
 #pragma unroll
-      for (int n = 0; n < AHEAD; ++n) {
-        mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], o));
-        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], o);
-      }
+      for (int n = 0; n < AHEAD; ++n) mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], o));
+    }
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      const float2 s = block_scale(mx[n]);
+      v[n] = make_float4(v[n].x * s.x, v[n].y * s.x, v[n].z * s.x, v[n].w * s.x);
+      sum[n] = (v[n].x + v[n].y) + (v[n].z + v[n].w);
+      back[n] = s.y;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], o);
     }
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
@@ -224,7 +237,7 @@ __device__ __forceinline__ void stage_x(const MvArgs& p, int t0, int nv, uint8_t
         const float a = __shfl_sync(0xffffffffu, v[n].x, next), b = __shfl_sync(0xffffffffu, v[n].y, next);
         if (va[n] % 64 < 32) v[n] = make_float4(v[n].z, v[n].w, a, b);
       }
-      if (vv[n] < nv) put_x<RT, C>(v[n], mx[n], sum[n], vv[n], va[n], xf, info);
+      if (vv[n] < nv) put_x<RT, C>(v[n], back[n], sum[n], vv[n], va[n], xf, info);
     }
   }
 }
@@ -497,12 +510,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float s = fmaf(h[2 * r] + h[2 * r + 1], 0.0625f, c[2 * r] + c[2 * r + 1]);
-              if (is_q4_0(RT)) {  // d (sum q x - 8 sum x)
-                acc[0][0][r] = fmaf(dd[r], fmaf(xin[qq].x, s, xin[qq].y), acc[0][0][r]);
-              } else {
-                acc[0][0][r] = fmaf(dd[r] * xin[qq].x, s, acc[0][0][r]);
-                acc[0][0][r] = fmaf(mm[r], xin[qq].y, acc[0][0][r]);
-              }
+              // (Q4_0: d (sum q x - 8 sum x))
+              const float u = is_q4_0(RT) ? dd[r] * (s + xin[qq].y) : fmaf(dd[r], s, mm[r] * xin[qq].y);
+              acc[0][0][r] = fmaf(xin[qq].x, u, acc[0][0][r]);
             }
           }
         } else {
@@ -550,8 +560,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   const float s = C::PARTS == 2 ? c[2 * r] + c[2 * r + 1] : c[2 * r + v];
-                  acc[n][v][r] = fmaf(d[r] * in.x, s, acc[n][v][r]);
-                  acc[n][v][r] = fmaf(m[r], in.y, acc[n][v][r]);
+                  acc[n][v][r] = fmaf(in.x, fmaf(d[r], s, m[r] * in.y), acc[n][v][r]);
                 }
               }
             }
