@@ -13,13 +13,16 @@
 // is one operand for two products, S^T comes from tensor memory without a pass through
 // shared memory, and a thread owns a piece of a row of S^T in f32 registers.
 //
-// Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; an
-// f32 one becomes two f16 parts (22 bits) of its value times a power of two for the chunk's
-// tile. Scores and the state as an operand keep two parts (16 bits in bf16, 22 in f16). The
-// decayed keys are summed into the f32 state, so they keep more bits for bf16 too: three
-// bf16 parts (24) or two f16 ones. f16 parts need their values in f16's range: scores and
-// states are scaled by a power of two for each row, decayed keys for each chunk. The product
-// of two low parts is left out. Sums, statistics and the state are f32.
+// Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; f32
+// ones, and their scores, decayed keys and states as operands, are three bf16 parts, which are the
+// f32 value whatever its neighbours are. (Two f16 parts of the value times a power of two for the
+// tile are half the products, prefill of 2 x 1024 tokens 64 us, but values far below the tile's
+// largest lose their bits: a document before a reset took those of the one behind it.) For 16-bit types
+// scores and the state as an operand keep two parts (16 bits in bf16, 22 in f16). The decayed keys
+// are summed into the f32 state, so they keep more bits for bf16 too: three bf16 parts or
+// two f16 ones. f16 parts need their values in f16's range: scores and states are scaled by a
+// power of two for each row, decayed keys for each chunk. Products of parts below the last kept
+// bit are left out. Sums, statistics and the state are f32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -42,15 +45,16 @@ __host__ __device__ constexpr uint32_t p_pitch(int i) { return 16u * (64 - 16 * 
 
 template <int NP>
 struct Plan {
-  static constexpr int NPP = 2;  // parts of scores and state operands
+  static constexpr int NPP = NP == 1 ? 2 : 3;  // parts of scores and state operands
   static constexpr uint32_t Q = 0, K = NP * TILE, V = 2 * NP * TILE, KT = 3 * NP * TILE;
-  static constexpr uint32_t P = KT + (NP == 1 ? 3 : 2) * TILE;
+  static constexpr uint32_t P = KT + 3 * TILE;
   static constexpr uint32_t MISC = P + NPP * PTILE;
   // NP 1: 114,560 bytes and 1,024 of slack, two CTAs an SM
-  static constexpr uint32_t BYTES = MISC + (NP == 1 ? 6016 : 7424);
-  // Tensor memory columns: scores then O1, O2, and the state's parts, [dk / 64][part][32]; A takes
-  // their place once O2 is done (a thread's columns of A are its columns of the parts).
-  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = 128, T_COLS = 256;
+  static constexpr uint32_t BYTES = MISC + (NP == 1 ? 6016 : 7296);
+  // Tensor memory columns: scores then O1, O2, and the state's parts, [warpgroup][part]; where there
+  // are two of them A takes their place once O2 is done (a thread's columns of A are its columns of
+  // the parts).
+  static constexpr uint32_t T_O1 = 0, T_O2 = 64, T_S = 128, T_A = NP == 1 ? 128 : 320, T_COLS = NP == 1 ? 256 : 512;
 };
 
 struct Decays {
@@ -74,7 +78,7 @@ struct Misc {
   int scratch[UNIT_SCRATCH];
   // f16: largest magnitudes on the way to the scales, and the scores' inverse scales
   alignas(16) float pinv[CH];
-  float kmax[8], smax[NWG][128], pmax[NWG][64], tmax[3][NWG * 4];  // tmax: f32 q, k, v by warp
+  float kmax[8], smax[NWG][128], pmax[NWG][64];
 };
 
 // bf16 (or f16) operands, K-major (0) or MN-major (1), f32 accumulator, shape M x N.
@@ -158,13 +162,16 @@ __device__ __forceinline__ float2 unpack(uint32_t u) {
   if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-// Two f32 values as n parts each, packed in pairs; the parts sum to the value to 8 n (f16: 11 n) bits.
+// Two f32 values as n parts each, packed in pairs; the parts sum to the value to 8 n (f16: 11 n) bits. The
+// first of three bf16 parts is cut off: they then are the value, and the largest numbers do not round
+// to an infinity.
 template <int n, bool F16 = false>
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t* out) {
 #pragma unroll
   for (int p = 0; p < n; ++p) {
     uint32_t h;
     if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    else if (n == 3 && p == 0) h = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
     out[p] = h;
     if (p + 1 < n) {
@@ -193,7 +200,7 @@ template <int pieces>
 __device__ __forceinline__ int piece_col(int i) { return ((threadIdx.x >> 8) * pieces + i) * 4; }
 
 // A thread's share of rows t0 .. t0 + n - 1 (zeros up to 64) of a [tokens][dim] f32 matrix:
-// 8-column pieces of one row, fetched early and put into the tile as two f16 parts when that
+// 8-column pieces of one row, fetched early and put into the tile as bf16 parts when that
 // is free. A warp's 32 pieces of one i fill four whole 128-byte lines.
 template <int NP, int PIECES>
 struct Loader {
@@ -215,32 +222,13 @@ struct Loader {
       }
     }
   }
-  // Largest finite magnitude of the warp's pieces: an infinity or a NaN stays one whatever the
-  // scale, and must not take the others' bits.
-  __device__ __forceinline__ float warp_max() const {
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(r[i][j]));
-    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-    if (mx > 3.402823466e38f) {
-      mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mx = isfinite(r[i][j]) ? fmaxf(mx, fabsf(r[i][j])) : mx;
-      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-    }
-    return mx;
-  }
-  __device__ __forceinline__ void put(uint8_t* dst, float scale) const {
+  __device__ __forceinline__ void put(uint8_t* dst) const {
     const int lane = threadIdx.x & 31, row = piece_row(), kc0 = piece_col<PIECES>(0) + (lane >> 3);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       uint32_t u[4][NP];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split_pair<NP, true>(r[i][2 * j] * scale, r[i][2 * j + 1] * scale, u[j]);
+      for (int j = 0; j < 4; ++j) split_pair<NP>(r[i][2 * j], r[i][2 * j + 1], u[j]);
       uint8_t* d = dst + piece(kc0 + i * 4, row);
 #pragma unroll
       for (int q = 0; q < NP; ++q)
@@ -385,9 +373,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
           uint32_t* ctrl) {
   using L = Plan<NP>;
   static_assert(sizeof(Misc<chunk_threads(NP) / 128>) <= L::BYTES - L::MISC, "misc");
-  constexpr bool F16 = !std::is_same<T, __nv_bfloat16>::value;  // the type of the parts
+  constexpr bool F16 = std::is_same<T, __half>::value;  // the type of the parts
   constexpr bool F32 = std::is_same<T, float>::value;
-  constexpr int NPP = L::NPP, LIM = 1;  // products of parts i, j with i + j <= LIM
+  constexpr int NPP = L::NPP, LIM = NPP - 1;  // products of parts i, j with i + j <= LIM
   constexpr int KP = F16 ? 2 : 3;       // parts of the decayed keys
   constexpr int NT = chunk_threads(NP), NWG = NT / 128;  // threads; warpgroups, which share rows
   constexpr int CPT = D / NWG, TPT = CH / NWG, SPT = 4 / NWG;  // a thread's columns of S, tokens, mask steps
@@ -453,10 +441,8 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     if (MODE == 1) tma_load_tile(sm + L::Q, &maps.q, a.dk, hq, begin, &m->full_q);
     tma_load_tile(sm + L::V, &maps.v, a.dv, h, begin, &m->full_v);
   }
-  // f32: a chunk's q, k and v on their way, and the scales (and their inverses) of their tiles
+  // f32: a chunk's q, k and v on their way
   Loader<NP, PIECES> lq, lk, lv;
-  float2 qsc = make_float2(1.f, 1.f), ksc = qsc, vsc = qsc;
-  float kmx = 0.f;
   auto fetch = [&](int t0) {
     if constexpr (F32) {
       const int n = min(CH, end - t0);
@@ -465,31 +451,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
       lv.fetch(v, a.vs, t0, n, a.dv);
     }
   };
-  auto write_max = [&]() {
+  auto put_qk = [&]() {
     if constexpr (F32) {
-      const float x = MODE == 1 ? lq.warp_max() : 0.f, y = lk.warp_max(), z = lv.warp_max();
-      if (lane == 0) m->tmax[0][warp] = x, m->tmax[1][warp] = y, m->tmax[2][warp] = z;
-    }
-  };
-  auto put_qk = [&]() {  // after a barrier behind write_max
-    if constexpr (F32) {
-      float mx[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mx[i] = fmaxf(mx[i], m->tmax[i][w]);
-      qsc = f16_scale(mx[0]);
-      ksc = f16_scale(mx[1]);
-      vsc = f16_scale(mx[2]);
-      kmx = mx[1];
-      if (MODE == 1) lq.put(sm + L::Q, qsc.x);
-      lk.put(sm + L::K, ksc.x);
+      if (MODE == 1) lq.put(sm + L::Q);
+      lk.put(sm + L::K);
     }
   };
   if (F32 && begin < end) {
     fetch(begin);
-    write_max();
-    __syncthreads();
     put_qk();
   }
   if (warp == 7) chunk_decays(a, h, begin, min(CH, end - begin), &m->d[0]);
@@ -613,16 +582,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     if constexpr (F32) {
       fence_proxy_async_smem();
       __syncthreads();  // q and k are there; the last chunk's outputs have left v's place
-      lv.put(tv, vsc.x);
+      lv.put(tv);
     }
     if (F32 || t0 == begin) issue_scores(ph);
     // ---- the decayed keys ---------------------------------------------------------------
     if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
-    if (!F16 && t0 == begin) __syncthreads();  // the first decays
+    if (NP == 1 && !F16 && t0 == begin) __syncthreads();  // the first decays (f32: above)
     float2 kscale = make_float2(1.f, 1.f);
-    if constexpr (F32) {
-      kscale = f16_scale(kmx * d->wmax);
-    } else if constexpr (F16) {
+    if constexpr (F16) {
       // largest finite magnitude, as packed f16 bits, of which the unsigned order is that of magnitudes
       auto largest = [&](auto keep) {
         uint32_t mx = 0;
@@ -650,7 +617,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     for (int i = 0; i < PIECES; ++i) {
       const int r = piece_row(), kc = piece_col<PIECES>(i) + (lane >> 3);
       if (piece_col<PIECES>(i) >= 2 * ks) break;
-      const float w = d->w[r] * kscale.x * ksc.y;
+      const float w = d->w[r] * kscale.x;
       float x[8];
       read_piece<NP, F16>(sm + L::K + tile_piece<NP>(kc, r), x);
       if (n < CH && r >= n) {  // rows past the chunk's tokens are other sequences' or none
@@ -716,7 +683,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
       ok = mbar_wait(&m->qk, ph) && ok;
       tc_fence_after_sync();
       const float4 gt = d->g[row];
-      const float qk = qsc.y * ksc.y, et = d->eg[row];
+      const float et = d->eg[row];
       uint32_t sc[SPT][16];
       float mx = 0.f;
 #pragma unroll
@@ -741,7 +708,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
           for (int j = 0; j < 16; ++j) {
             const float4 gs = d->g[step * 16 + j];
             const float x = ex2((gt.x - gs.x) + (gt.y - gs.y));
-            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * qk * x * a.scale) : 0u;
+            s[j] = gt.z == gs.z ? __float_as_uint(__uint_as_float(s[j]) * x * a.scale) : 0u;
           }
         }
         if (step >= 2 * quarter) {  // (rows 32 .. 63 see all of the first 32 columns)
@@ -804,10 +771,9 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     ok = mbar_wait(&m->end, ph) && ok;
     tc_fence_after_sync();
     if (MODE == 0) {
-      add_state(d->lam, kscale.y * vsc.y);
-      if (F32 && more) write_max();
+      add_state(d->lam, kscale.y);
+      if (more) put_qk();
       __syncthreads();  // the next decays are there
-      if (F32 && more) put_qk();
       continue;
     }
     // ---- outputs ----------------------------------------------------------------------
@@ -815,7 +781,6 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     // ones for 32-bit types, two halves of 64 channels otherwise.
     T* stage = reinterpret_cast<T*>(sm + L::V);
     constexpr int SW = sizeof(T) == 4 ? D : 64;  // channels of a staged row
-    const float s2 = sinv * qsc.y;
     float bad = 0.f;
 #pragma unroll
     for (int c = 0; c < TPT / 16; ++c) {
@@ -836,13 +801,12 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const float y1 = __uint_as_float(o1[j + f]), y2 = __uint_as_float(o2[j + f]);
-          const float x = F16 ? fmaf(ev[f], y2 * s2, y1 * (F32 ? pv[f] * vsc.y : pv[f])) : fmaf(ev[f], y2, y1);
+          const float x = F16 ? fmaf(ev[f], y2 * sinv, y1 * pv[f]) : fmaf(ev[f], y2, y1);
           bad = fmaf(x, 0.f, bad);
           stage[(row / SW) * CH * SW + (t + f) * SW + row % SW] = from_f32<T>(x);
         }
       }
     }
-    if (F32 && more) write_max();
     fence_proxy_async_smem();
     tc_fence_before_sync();
     // a sum of zeros unless a value is not finite (one of the rows past the chunk's tokens, then,
@@ -851,7 +815,6 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     tc_fence_after_sync();
     // the next chunk's scores may take O1's place: its q and k have come meanwhile
     if (!F32 && more) issue_scores(ph ^ 1);
-    const float ainv = kscale.y * vsc.y;
     if (more) put_qk();
     if (redo) {
       token_by_token(t0, n, d);
@@ -871,7 +834,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
                 *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(stage) + i * 16);
         }
       }
-      add_state(d->lam, ainv);
+      add_state(d->lam, kscale.y);
     }
     put_state();
     if (NP == 1 && iwarp && elect_one()) {
@@ -1033,7 +996,7 @@ cudaError_t linattn_chunk_launch(const LinattnArgs& a, int type, void* ws, bool 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool wide = a.dk > 112;
   if (type == MOE_F32)
-    return wide ? chunk_launch<float, 2, true>(a, type, w, pdl, st) : chunk_launch<float, 2, false>(a, type, w, pdl, st);
+    return wide ? chunk_launch<float, 3, true>(a, type, w, pdl, st) : chunk_launch<float, 3, false>(a, type, w, pdl, st);
   if (type == MOE_F16)
     return wide ? chunk_launch<__half, 1, true>(a, type, w, pdl, st) : chunk_launch<__half, 1, false>(a, type, w, pdl, st);
   return wide ? chunk_launch<__nv_bfloat16, 1, true>(a, type, w, pdl, st)
