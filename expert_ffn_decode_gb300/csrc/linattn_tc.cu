@@ -21,7 +21,8 @@
 // scores and the state as an operand keep two parts (16 bits in bf16, 22 in f16). The decayed keys
 // are summed into the f32 state, so they keep more bits for bf16 too: three bf16 parts or
 // two f16 ones. f16 parts need their values in f16's range: scores and states are scaled by a
-// power of two for each row, decayed keys for each chunk. Products of parts below the last kept
+// power of two for each row, decayed keys for each chunk, and keep their 22 bits down to 2^-15 of the
+// largest there, fewer below. Products of parts below the last kept
 // bit are left out. Sums, statistics and the state are f32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -66,8 +67,7 @@ struct Decays {
   float ghi, glo;    // sum over the chunk without resets
   int reset;         // whether the chunk forgets
   int mild;          // no resets, and every exp(G_t) within 2^-80 .. 2^20
-  float wmax;        // largest w
-  int pad[2];
+  int pad[3];
 };
 template <int NWG>  // warpgroups
 struct Misc {
@@ -326,20 +326,16 @@ __device__ __forceinline__ void chunk_decays(const LinattnArgs& a, int h, int t0
   const bool ok = fminf(ph, ch) > -80.f && fmaxf(ph, ch) < 20.f && ph == ph && ch == ch;
   const bool mild = __all_sync(0xffffffffu, ok) && er == 0;
   const float gh[2] = {ph, ch}, gl[2] = {pl, cl};
-  float wm = 0.f;
   const int gr[2] = {pr, cr};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int t = 2 * lane + j;
     m->g[t] = make_float4(gh[j], gl[j], (float)gr[j], expf(raw[j]));
     m->w[t] = gr[j] == er ? ex2((eh - gh[j]) + (el - gl[j])) : 0.f;
-    wm = fmaxf(wm, m->w[t]);
     m->eg[t] = gr[j] == 0 ? ex2(gh[j] + gl[j]) * a.scale : 0.f;
     m->ieg[t] = ex2(-(gh[j] + gl[j]));
   }
-  wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wm)));  // of non-negative numbers
   if (lane == 0) {
-    m->wmax = wm;
     m->lam = er == 0 ? ex2(eh + el) : 0.f;
     m->ghi = eh;
     m->glo = el;
@@ -587,31 +583,36 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
     if (F32 || t0 == begin) issue_scores(ph);
     // ---- the decayed keys ---------------------------------------------------------------
     if (NP == 1) ok = mbar_wait(&m->full_k, ph) && ok;
-    if (NP == 1 && !F16 && t0 == begin) __syncthreads();  // the first decays (f32: above)
+    if (NP == 1 && t0 == begin) __syncthreads();  // the first decays (f32: above)
     float2 kscale = make_float2(1.f, 1.f);
     if constexpr (F16) {
-      // largest finite magnitude, as packed f16 bits, of which the unsigned order is that of magnitudes
+      // The largest finite magnitude of what a token's key is after its decay: of the lane's row of k, as
+      // packed f16 bits, of which the unsigned order is that of magnitudes, times the row's own decay
+      // (a key that a reset or a strong decay leaves nothing of must not take the others' bits).
+      const int r = piece_row();
       auto largest = [&](auto keep) {
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          const int r = piece_row(), kc = piece_col<PIECES>(i) + (lane >> 3);
+          const int kc = piece_col<PIECES>(i) + (lane >> 3);
           if (r < n && kc < 2 * ks) {
             const uint4 u = *reinterpret_cast<const uint4*>(sm + L::K + tile_piece<NP>(kc, r));
             mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(keep(u.x & 0x7fff7fffu), keep(u.y & 0x7fff7fffu)),
                                        __vmaxu2(keep(u.z & 0x7fff7fffu), keep(u.w & 0x7fff7fffu))));
           }
         }
-        return __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+        return max(mx & 0xffffu, mx >> 16);
       };
       uint32_t mx = largest([](uint32_t u) { return u; });
-      if (mx >= 0x7c00u) mx = largest([](uint32_t u) { return u & __vcmpltu2(u, 0x7c007c00u); });
-      if (lane == 0) m->kmax[warp] = __half2float(__ushort_as_half((unsigned short)mx));
-      __syncthreads();  // also: the first decays
+      if (__any_sync(0xffffffffu, mx >= 0x7c00u)) mx = largest([](uint32_t u) { return u & __vcmpltu2(u, 0x7c007c00u); });
+      const float decayed = __half2float(__ushort_as_half((unsigned short)mx)) * d->w[r];
+      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(decayed));  // of non-negative numbers
+      if (lane == 0) m->kmax[warp] = __uint_as_float(most);
+      __syncthreads();
       float km = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) km = fmaxf(km, m->kmax[i]);
-      kscale = f16_scale(km * d->wmax);
+      kscale = f16_scale(km);
     }
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
