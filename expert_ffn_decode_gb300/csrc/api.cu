@@ -687,6 +687,9 @@ void clear_graphs() {
 int status_error(uint32_t bits) {
   if (bits & moe::DEV_ERR_MBAR_TIMEOUT)
     return fail(MOE_ERR_TIMEOUT, "a device-side wait timed out (status bits 0x%x); control block reset", bits);
+  if (bits & moe::DEV_ERR_OFFSETS)
+    return fail(MOE_ERR_INVALID_CFG, "offsets that go back and rise again make long sequences share tokens (status bits "
+                "0x%x): sequences without room kept their state and rows; control block reset", bits);
   return fail(MOE_ERR_WORKSPACE,
               "a decode pick in the workspace was out of range (status bits 0x%x): the workspace was not "
               "zero-filled before its first use; control block reset", bits);

@@ -21,6 +21,7 @@ constexpr int CTRL_BYTES = 512;
 enum DevErr : uint32_t {
   DEV_ERR_MBAR_TIMEOUT = 2u,   // a copy or a slot release never arrived
   DEV_ERR_BAD_PICK = 4u,       // a decode pick read from the workspace was out of range
+  DEV_ERR_OFFSETS = 8u,        // prompts' offsets ask for more units than the call's tokens have
 };
 
 // Raises a kernel's dynamic shared memory limit on the current device when a launch needs

@@ -27,7 +27,7 @@ __device__ __forceinline__ int seq_slot(const LinattnArgs& a, int b) {
 __host__ __device__ __forceinline__ int seq_units(int n, int seg) { return n > seg ? (n + seg - 1) / seg : 1; }
 
 struct Unit {
-  int b;      // sequence
+  int b;      // sequence, or -1: the call has no such unit
   int i, n;   // unit i of n
   int seg;    // tokens of a unit
   int slot0;  // workspace state of the sequence's unit 0 (sequences of several units)
@@ -38,9 +38,9 @@ constexpr int UNIT_SCRATCH = 4 + 3 * 8;  // ints of shared memory that find_unit
 // others, each of seg tokens, in sequence order. Of up to 256 sequences the last units of more
 // than half of seg come first (`by_rank`), so that a grid in this order ends with its shortest
 // pieces. A whole CTA (256 threads of it) settles whether the call stays whole, where that is
-// open, and adds up what the sequences before u's have. `n_ws`: states in the workspace; a
-// sequence whose units would not fit (offsets that descend can make sequences share tokens) is
-// not found.
+// open, and adds up what the sequences before u's have. `n_ws`: states in the workspace. Offsets that
+// go back and rise again make sequences share tokens and have more units than the call's tokens: a
+// sequence whose states do not fit, or whose units are not all launched, is not found (b stays).
 __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, int n_ws, int u, int* scratch,
                                           bool by_rank = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,7 +118,7 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, 
       scratch[0] = b;
       scratch[1] = u < a.B ? nu : u - a.B - pu;
       scratch[2] = nu + 1;
-      scratch[3] = ps;
+      scratch[3] = ps + nu + 1 <= n_ws && pu + nu <= cut.rest ? ps : -1;
     }
     if (u < a.B ? u < b0 + 256 : u - a.B < base_u) break;
   }
@@ -127,7 +127,7 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, 
   r.i = scratch[1];
   r.n = scratch[2];
   r.slot0 = scratch[3];
-  r.found = r.b >= 0 && (r.n == 1 || r.slot0 + r.n <= n_ws);
+  r.found = r.b >= 0 && (r.n == 1 || r.slot0 >= 0);
   __syncthreads();  // scratch may be reused
   return r;
 }

@@ -385,14 +385,14 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
   // of any length, fill what is left (143 -> 120 us for a ragged batch of 9 prompts); the state
   // pass has no last units.
   const int h = blockIdx.x % a.H, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
-  const int whole = (int)(gridDim.x / a.H) - a.B, at = blockIdx.x / a.H;  // MODE 1: units but the last, at most
-  const int u = MODE == 0 || at < whole ? a.B + at : at - whole;
+  const int at = blockIdx.x / a.H, u = MODE == 0 || at < cut.rest ? a.B + at : at - cut.rest;
   // Behind the join everything but the states is older than the state pass, which has ended: this
   // grid then sets up and loads its first chunk beside the join and waits for the states alone.
   if (!behind_join) pdl_wait_prior_grids();
   const Unit un = find_unit(a, cut, n_ws, u, m->scratch);
   if (!un.found) {
     if (behind_join) pdl_wait_prior_grids();  // no grid ends before the one it stands behind
+    if (MODE == 1 && u < a.B && h == 0 && tid == 0) atomicOr(ctrl + CTRL_STATUS, DEV_ERR_OFFSETS);
     return;
   }
   int begin, end;
@@ -963,7 +963,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int t
 
 template <typename T, int NP, bool WIDE>
 cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, cudaStream_t st) {
-  const LinattnSplit sp = linattn_split(a.N, a.offsets ? a.N : a.seq_len, a.B, a.H, type);
+  LinattnSplit sp = linattn_split(a.N, a.offsets ? a.N : a.seq_len, a.B, a.H, type);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(ws);
   float* wd = reinterpret_cast<float*>(ws + sp.decays);
   float* wst = reinterpret_cast<float*>(ws + sp.states);
@@ -977,18 +977,18 @@ cudaError_t chunk_launch(const LinattnArgs& a, int type, uint8_t* ws, bool pdl, 
     if ((e = make_map(&maps.o, a.o, a.dv, a.H, a.N, a.os, false)) != cudaSuccess) return e;
   }
   const int smem = Plan<NP>::BYTES + 1024;  // 1,024-byte alignment
-  const int whole = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.cut.seg * a.B;  // units but the last, at most
-  if (whole > 0) {
-    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)whole * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws, 0, wd,
+  const int rest = sp.cut.rest = a.offsets ? sp.units - a.B : (a.seq_len - 1) / sp.cut.seg * a.B;
+  if (rest > 0) {
+    e = launch(lin_chunk<T, NP, 0, WIDE>, dim3((unsigned)rest * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws, 0, wd,
                wst, ctrl);
     if (e != cudaSuccess) return e;
-    const int by_seq = a.B <= whole;
-    const dim3 jgrid((unsigned)(by_seq ? a.B : whole), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
+    const int by_seq = a.B <= rest;
+    const dim3 jgrid((unsigned)(by_seq ? a.B : rest), (unsigned)a.H, (unsigned)((a.dk * a.dv + 2047) / 2048));
     e = launch(lin_join, jgrid, 256, 0, pdl, st, a, sp.cut, sp.n_ws, by_seq, (const float*)wd, wst);
     if (e != cudaSuccess) return e;
   }
-  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(whole + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws,
-                whole > 0 ? 1 : 0, wd, wst, ctrl);
+  return launch(lin_chunk<T, NP, 1, WIDE>, dim3((unsigned)(rest + a.B) * a.H), chunk_threads(NP), smem, pdl, st, a, maps, sp.cut, sp.n_ws,
+                rest > 0 ? 1 : 0, wd, wst, ctrl);
 }
 
 }  // namespace

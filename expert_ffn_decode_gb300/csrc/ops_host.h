@@ -60,7 +60,8 @@ struct LinattnArgs {
 constexpr int LINATTN_MIN_SEG = 128;
 struct LinattnCut {
   int seg, whole;
-  int ask;  // whether to stay whole is up to the offsets
+  int ask;   // whether to stay whole is up to the offsets
+  int rest;  // units but the sequences' last ones that are launched
 };
 struct LinattnSplit {
   LinattnCut cut;
@@ -83,7 +84,7 @@ inline LinattnSplit linattn_split(int N, int longest, int B, int H, int type) {
   if (seg > 1 << 28) seg = 1 << 28;
   const int64_t whole = linattn_whole(seg, type);
   if (longest <= whole) seg = whole;
-  s.cut = {(int)seg, (int)whole, longest > whole && (longest + B - 1) / B <= whole};
+  s.cut = {(int)seg, (int)whole, longest > whole && (longest + B - 1) / B <= whole, 0};
   const int cuts = longest <= whole ? 0 : N / s.cut.seg;
   s.units = cuts + B;         // sum of ceil(n_b / seg), an empty sequence counting one
   s.n_ws = 2 * cuts;          // a sequence longer than seg has at most 2 n_b / seg units

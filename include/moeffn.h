@@ -228,8 +228,9 @@ size_t moe_workspace_size(const moe_cfg* cfg);
 size_t moe_trace_offset(const moe_cfg* cfg);
 
 /* Waits for `stream`, then reads and clears the workspace's status word:
- * MOE_OK, or MOE_ERR_TIMEOUT when a device-side wait ran out of time (the
- * workspace's control block is zeroed again so it can be reused). */
+ * MOE_OK, or MOE_ERR_TIMEOUT when a device-side wait ran out of time, or
+ * MOE_ERR_INVALID_CFG when offsets left sequences without room (moe_linattn_prefill); the
+ * workspace's control block is zeroed again so it can be reused. */
 int moe_workspace_status(void* workspace, void* stream);
 
 /* Exercises the error path above without a fault: one kernel waits on an mbarrier that
@@ -344,7 +345,10 @@ typedef struct moe_linattn_cfg {
 
 /* Whole prompts: sequence b is the tokens offsets[b] .. offsets[b + 1] - 1 (device int32,
  * n_seq + 1 values, ascending; bounds outside 0 .. n_tokens are clamped to it and a
- * descending pair is an empty sequence). offsets NULL: n_seq sequences of n_tokens / n_seq
+ * descending pair is an empty sequence; where they then rise again, sequences share tokens:
+ * what their common rows of o hold is open, and long sequences for which the call has no units
+ * keep their state and rows, which moe_workspace_status reports as MOE_ERR_INVALID_CFG).
+ * offsets NULL: n_seq sequences of n_tokens / n_seq
  * tokens. An empty sequence keeps its state (or gets a zero one with MOE_FRESH_STATE).
  * Rows of o that no sequence covers are not written. `workspace` as for
  * moe_ffn_forward_ex (zero-filled before its first use, then this library's), of at
