@@ -45,7 +45,14 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, 
                                           bool by_rank = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool ranked = by_rank && a.B <= 256;
-  int first = 0, past = 0, seg = cut.seg;  // of sequence tid
+  int seg = cut.seg, begin_u = 0, end_u = 0;
+  const bool own = u < a.B && (a.B == 1 || !ranked);  // the last unit of sequence u
+  if (own) {
+    seq_range(a, u, begin_u, end_u);
+    // whole by its own length: nothing of the other sequences matters, however many there are
+    if (end_u - begin_u <= seg) return Unit{u, 0, 1, seg, 0, true};
+  }
+  int first = 0, past = 0;  // of sequence tid
   if (tid < min(256, a.B)) seq_range(a, tid, first, past);
   if (cut.ask) {
     int longest = past - first;
@@ -61,11 +68,9 @@ __device__ __forceinline__ Unit find_unit(const LinattnArgs& a, LinattnCut cut, 
     if (longest <= cut.whole) seg = cut.whole;
   }
   Unit r{0, 0, 1, seg, 0, true};
-  if (u < a.B && (a.B == 1 || !ranked)) {
-    int begin, end;
-    seq_range(a, u, begin, end);
+  if (own) {
     r.b = u;
-    r.n = seq_units(end - begin, seg);
+    r.n = seq_units(end_u - begin_u, seg);
     r.i = r.n - 1;
     if (r.n == 1) return r;
   }

@@ -874,11 +874,6 @@ __global__ void __launch_bounds__(256) lin_join(LinattnArgs a, LinattnCut cut, i
   __shared__ int scratch[UNIT_SCRATCH];
   pdl_wait_prior_grids();
   pdl_launch_dependents();  // the output pass may set up
-  if (by_seq) {  // most calls' sequences are whole
-    int begin, end;
-    seq_range(a, blockIdx.x, begin, end);
-    if (end - begin <= cut.seg) return;
-  }
   const Unit un = find_unit(a, cut, n_ws, by_seq ? blockIdx.x : a.B + blockIdx.x, scratch, false);
   if (!un.found || un.n == 1 || (!by_seq && un.i != 0)) return;
   const int slot = seq_slot(a, un.b);

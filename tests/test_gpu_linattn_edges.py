@@ -68,3 +68,16 @@ def test_short_sequences_that_share_tokens(type, n):
         _, s, _, a = oracle_range(c, i, j, before[b])
         assert np.all(np.abs(got[b] - s) <= (2 * n + c.dk + 64) * 2.0 ** -24 * a)
     assert np.array_equal(got[1], before[1])
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("longest", [300, 700])
+def test_thousands_of_sequences(type, longest):
+    """Far more sequences than one round of the search takes, with and without some that are cut."""
+    rng = np.random.default_rng(51)
+    lens = [int(n) for n in rng.integers(0, 4, 3000)]
+    for b in (0, 255, 256, 1999, 2999):
+        lens[b] = longest
+    c = Case(lens, H=2, G=1, dk=16, dv=24, type=type, decay="reset")
+    want = c.want()
+    c.check(c.prefill(), c.state, want)
