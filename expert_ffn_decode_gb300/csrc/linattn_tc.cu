@@ -25,12 +25,12 @@
 // largest there, fewer below. Products of parts below the last kept
 // bit are left out. Sums, statistics and the state are f32.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <type_traits>
 
 #include "linattn.cuh"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
@@ -937,15 +937,8 @@ cudaError_t launch(K kern, dim3 grid, int threads, int smem, bool pdl, cudaStrea
 // A [tokens][heads][dim] tensor of 16-bit values in boxes of 64 tokens x 64 columns of one head, rows of
 // 128 bytes, in the 128-byte swizzle for operands and as they are for outputs.
 cudaError_t make_map(CUtensorMap* m, const void* base, int dim, int heads, int tokens, int64_t stride, bool swizzle) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r{};
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
-    if (e != cudaSuccess) return e;
-    if (r != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
+  const auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
   const cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};

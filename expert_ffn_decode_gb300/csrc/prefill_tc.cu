@@ -29,7 +29,6 @@
 // Every stage wait is bounded; a timeout anywhere stops every role of the CTA and
 // sets the status word.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
@@ -39,6 +38,7 @@
 #include "plan.h"
 #include "prefill_host.h"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
@@ -1049,23 +1049,10 @@ __global__ void __launch_bounds__(256) tile_images(const PrefillArgs a, int rout
 }
 
 // ---- host side -----------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // 2-D map over `rows` rows of `row_bytes` bytes (u8 elements) or f32 elements.
 cudaError_t encode_2d(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows, uint32_t box_x,
                       uint32_t box_y, bool swizzle128) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {inner * (f32 ? 4 : 1)};
@@ -1094,7 +1081,7 @@ cudaError_t launch_tile(const PrefillArgs& a, const TileMaps& maps, cudaStream_t
 // not be a whole number of them); boxes of box_x bytes x box_y rows x 1 block.
 cudaError_t encode_3d(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t n,
                       uint64_t stride2, uint32_t box_x, uint32_t box_y) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {row_bytes, rows, n};
   const cuuint64_t strides[2] = {row_bytes, stride2};
