@@ -1,4 +1,4 @@
-"""A whole recurrent decoder layer on one GPU: a prompt, then tokens one at a time.
+"""A recurrent decoder layer with one decay a head on one GPU: a prompt, then tokens one at a time.
 
     python examples/linear_layer.py [--prompt 300] [--tokens 16] [--sequences 4] [--check]
 

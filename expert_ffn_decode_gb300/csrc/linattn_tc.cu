@@ -382,7 +382,7 @@ lin_chunk(LinattnArgs a, const __grid_constant__ Maps maps, LinattnCut cut, int 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, quarter = warp & 3;
   const bool iwarp = __shfl_sync(0xffffffffu, warp, 0) == 3;  // whose elected lane issues
   // The heads of a unit are neighbours. Whole units come first and the sequences' last ones,
-  // of any length, fill what is left (143 -> 120 us for a ragged batch of 9 prompts); the state
+  // of any length, fill what is left (143 -> 120 us for a ragged batch of 9 f16 prompts); the state
   // pass has no last units.
   const int h = blockIdx.x % a.H, row = quarter * 32 + lane;  // row: this thread's lane of tensor memory
   const int at = blockIdx.x / a.H, u = MODE == 0 || at < cut.rest ? a.B + at : at - cut.rest;

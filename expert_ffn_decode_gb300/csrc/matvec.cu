@@ -6,9 +6,10 @@
 // -dmin mn), so a nibble is used as the integer it is and never rounded. The inner sum runs on
 // the tensor cores by mma.m16n8k16, whose operands are registers: at one vector there is a
 // matrix row of work for one accumulator column, far too little for a tcgen05 tile. Bytes are the
-// floor and instructions what is left over it: 128,000 x 2048 Q4_0 and one vector take 33.6 us
-// (66% of HBM's rate; 2.9 instructions a weight, the schedulers 62% busy, half of it nibbles; one
-// warp a row with f32 products 888 us). A pair of nibbles becomes an f16 operand by one AND (the
+// floor: 128,000 x 2048 Q4_0 and one vector take 33.8 us (65% of HBM's rate; one warp a row
+// with f32 products 888 us). Nothing is full: 2.9 instructions a weight issue in 62% of the slots,
+// ALU 40%, DRAM 50%. What is left over the floor is the latency of each warp's chain from shared
+// memory through nibbles, products and scales with 16 warps an SM (124 registers a thread). A pair of nibbles becomes an f16 operand by one AND (the
 // bits of a nibble in the low bits of an f16 are the subnormal q 2^-24, or 16 q 2^-24 for the
 // high one) and one multiplication by a power of two to q 2^-10. The multiplication is
 // needed for the sums, not for the values: a subnormal operand counts in the accumulator's
@@ -54,7 +55,7 @@ struct Cols {
   static constexpr int VECS = MULTI ? 8 * NT / PARTS : 1;
   static constexpr int JOIN = MULTI ? VECS : 2;  // tiles of 16 sums a warp puts up at a time
   static constexpr int XBYTES = MULTI ? 16 * NT : 4;  // bytes of x pieces for each of a row's values
-  // Warps of a CTA and stages of a warp's ring (all but one in flight). Several vectors' x pieces
+  // Warps of a CTA and stages of a warp's ring. Several vectors' x pieces
   // leave room for one CTA an SM, which then has sixteen warps to share them (8192 x 2560, eight
   // vectors: 10.8 us, 12.5 with eight), or eight where longer rows leave no more room.
   static constexpr int WARPS = WARPS_, DEPTH = MULTI ? 2 : 4;
@@ -265,8 +266,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int byt
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// A warp's steps: the tiles of its group in turn, and in each its range of runs. Each step's rows are copied to the warp's own ring, three steps ahead, so a
-// warp never waits for another one but to join the partial sums of a tile.
+// A warp's steps: the tiles of its group in turn, and in each its range of runs. Each step's rows are
+// copied to the warp's own ring, so a warp never waits for another one but to join the partial sums
+// of a tile. A step's products come before the copy into the stage that the step before it left: with
+// DEPTH stages DEPTH - 2 copies are in flight beside the products, two for one vector and none for
+// several, where the other warps' products are what hides them.
 template <int RT, class C>
 __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel(const __grid_constant__ MvArgs p) {
   extern __shared__ __align__(128) uint8_t sm[];
@@ -291,8 +295,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MULTI ? 1 : 2) matvec_kernel
   // ---- weights: the copies of one step -----------------------------------------------
   // The 16 rows' windows in 16-byte pieces, consecutive pieces on consecutive lanes: an
   // instruction then touches few lines (four lanes a row, eight rows at once, are fewer
-  // instructions and slower: 33.6 -> 36.9 us for the 128,000 x 2048 head). Tiles and full runs start at multiples of 16 bytes,
-  // so where a lane's pieces are within them never changes.
+  // instructions and slower: 33.6 -> 36.9 us for the 128,000 x 2048 head). Tiles and full runs
+  // start at multiples of 16 bytes, so where a lane's pieces are within them never changes.
   constexpr int PIECES = RT == ROW_Q4_K || RT == ROW_PLANES ? RUN / 16 : RUN / 16 + 1;
   constexpr int TURNS = (16 * PIECES + 31) / 32;
   int from[TURNS], to[TURNS];  // a piece's place in the tile's bytes (run 0) and in the stage
@@ -673,8 +677,9 @@ bool try_launch(MvArgs& p, cudaStream_t st, cudaError_t* e) {
 // them, up to sixteen, but keeps x pieces for each: 16 bytes a value for four f32 vectors or
 // eight of 16 bits. Rows too long for that (about 2,000 values for sixteen f32 vectors, 5,000
 // for eight, 10,000 for four; twice that in 16 bits) take fewer vectors a pass, in the end one.
-// (8192 x 2048: sixteen f32 vectors 15.1 us in one pass of eight warps, 16.6 in two of sixteen;
-// sixteen bf16 ones 11.3 and 14.9.)
+// (8192 x 2048: sixteen f32 vectors 15.4 us in one pass of eight warps, 16.6 in two of sixteen;
+// sixteen bf16 ones 11.3 and 14.9.) There is no form for more vectors than that: every further
+// sixteen read and unpack the matrix again (8192 x 2560 Q4_1, bf16: 16 vectors 14.8 us, 64 56, 512 380).
 template <int RT>
 cudaError_t launch_cols(MvArgs& p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;

@@ -50,9 +50,10 @@ struct LinattnArgs {
 // costs a second pass over k and v, a state's round trip and two launches, so a call stays whole
 // if its longest sequence has no more than `whole` tokens, which then take no longer in one
 // piece than two passes over `seg`. One sequence with 16 heads of 128 in bf16 takes 21 us whole
-// and 24 cut at 320 tokens, 30 and 25 at 512, 56 and 27 at 1024 (f32: 47 and 47 at 256, 57 and 46
-// at 320); 8 sequences of 512 tokens 35 and 51, 16 of 448 43 and 92; units of 128 tokens against
-// 256 take 25 and 35 us at 512, 52 and 50 at 4096.
+// and 24 cut at 320 tokens, 30 and 25 at 512, 56 and 27 at 1024 (f16 on the same line, which it
+// crosses earlier: 26 and 28 at 320, 30 and 28 at 384; f32 46 and 44 at 256, 57 and 43 at 320);
+// 8 sequences of 512 tokens 35 and 51, 16 of 448 43 and 92; units of 128 tokens against
+// 256 take 25 and 35 us at 512, 52 and 50 at 4096. All measured with 16 heads of 128.
 // `longest` bounds a sequence's tokens: with offsets the host knows the total alone, and where
 // that leaves it open the kernels look (`ask`).
 // `units` bounds the units' number, `n_ws` the states that sequences of several units keep in the

@@ -267,8 +267,9 @@ int moe_ffn_forward_noalloc(const float* x, const float* router_w, const float* 
 
 /* ---------------------------------------------------------------------------------------
  * Operators next to the step: the projections of a layer whose matrices are 4-bit blocks,
- * and linear attention with a decay for each head. With the step they make a whole
- * recurrent layer: projection, moe_linattn_prefill or moe_linattn_step, projection added
+ * and linear attention with a decay for each head (one number a head and token; no decay
+ * for each key channel and no delta rule). With the step they make a whole recurrent layer
+ * of that kind: projection, moe_linattn_prefill or moe_linattn_step, projection added
  * into the residual stream, moe_ffn_forward_ex with the norm prologue and MOE_RESIDUAL
  * (examples/linear_layer.py).
  * ------------------------------------------------------------------------------------- */
@@ -299,10 +300,16 @@ typedef struct moe_matvec_cfg {
 } moe_matvec_cfg;
 
 /* y_t = W x_t (+ bias) (+ y_t) for n_vec vectors, enqueued on `stream`. `bias` is [rows] f32
- * or NULL; scales and mins are NULL unless qtype is MOE_Q4_PLANES. No workspace. Sums are
- * f32 or wider whatever the types, y is rounded once, and repeat calls agree bit for bit. Each
- * vector's result does not depend on the others of the call. A vector that holds an
- * infinity or a NaN gives rows that are not finite.
+ * or NULL; scales and mins are NULL unless qtype is MOE_Q4_PLANES. No workspace. Weights
+ * enter as they are. x enters in 22 bits (two f16 parts) of each value down to 2^-15 of the
+ * largest of its block of 32, fewer below (f16 and bf16 values as they are down to 2^-27).
+ * Sums are f32, y is rounded once, and repeat calls agree bit for bit. Each vector's result
+ * does not depend on the others of the call (their number picks the order of the sums). A
+ * vector that holds an infinity or a NaN gives rows that are not finite.
+ * A call reads the matrix once for up to 16 vectors (fewer where rows are long) and again for
+ * every further 16, so it is not the form for long prompts: with torch, dequantising
+ * 8192 x 2560 and one library product take less time from about 350 bf16 vectors (600 f32
+ * ones) on, and where the dequantised matrix is kept from a handful (70 f32 ones) on.
  * The matrix is read before the previous kernel on the stream has finished, as the step
  * reads its weights, unless MOE_NO_PDL is set. Alignment: weights, scales, mins, x and every
  * vector of x (x_stride) 16 bytes; y and bias their element. x and y must not overlap. */
@@ -316,7 +323,8 @@ int moe_q4_matvec(const void* x, const void* weights, const void* scales, const 
  *   q, k       [n_tokens][n_qk_heads][key_dim]; head h reads q/k head h / (n_heads / n_qk_heads)
  *   v, o       [n_tokens][n_heads][value_dim]
  *   log_decay  g, f32: [n_heads], or [n_tokens][n_heads] with MOE_TOKEN_DECAY. -infinity
- *              forgets the state before the token.
+ *              is a factor of 0: it forgets the finite state before the token (an infinity or a
+ *              NaN stays one as a NaN; MOE_FRESH_STATE takes no notice of either).
  *   state      [n_states][n_heads][key_dim][value_dim] f32, updated in place
  *   slots      [n_seq] int32, the state of each sequence, or NULL for sequence b in state b.
  *              A sequence whose slot is outside 0 .. n_states - 1 is inactive: its rows of o
@@ -353,7 +361,16 @@ typedef struct moe_linattn_cfg {
  * Rows of o that no sequence covers are not written. `workspace` as for
  * moe_ffn_forward_ex (zero-filled before its first use, then this library's), of at
  * least moe_linattn_workspace_size(cfg) bytes; a wait that gave up surfaces through
- * moe_workspace_status. */
+ * moe_workspace_status.
+ * Bits: sums, decays and states are f32, o is rounded once. Short prompts multiply in f32.
+ * Longer ones multiply on the tensor cores: f32 values, scores and states as they are (24
+ * bits each, whatever stands beside them); f16 and bf16 q, k, v as they are, with bf16's
+ * scores and states in 16 bits and its decayed keys in 24, and f16's scores, states and
+ * decayed keys in 22 bits down to 2^-15 of the largest beside them, fewer below (of a token's
+ * scores, of a value channel's state, of the decayed keys of 64 tokens).
+ * A value that is not finite reaches what the formula gives it and no earlier token, no other
+ * sequence and no other head. Chunks of 64 tokens with such an output are redone token by
+ * token, so a head whose state holds one takes several times as long from there on. */
 int moe_linattn_prefill(const void* q, const void* k, const void* v, const float* log_decay,
                         const int32_t* offsets, const int32_t* slots, const moe_linattn_cfg* cfg, float* state,
                         void* o, void* workspace, size_t workspace_bytes, void* stream);
