@@ -229,9 +229,12 @@ bool scan_few(const LinattnArgs& a) { return (int64_t)a.B * a.H * ((a.dv + 15) /
 // Whether walking the tokens is quicker than chunks, by what each takes in ns at widths of 128
 // (heads: of all sequences). The walk: launch, the states both ways, each token of the longest
 // sequence and, where heads fill the SMs, each token of each head. Chunks: a chain of them for
-// a sequence, or waves of heads. Measured, us, walk / bf16 chunks (f32 chunks):
-//   tokens x heads    32 x 16: 5.2 / 10.1 (13.6)   64 x 16: 9.0 / 9.8 (15.7)   128 x 16: 16.2 / 13.0 (24.3)
-//                     32 x 64: 10.2 / 10.7   32 x 256: 28 / 14.5 (28.5)   4 x 2048: 70 / 92   16 x 2048: 124 / 95
+// a sequence, or waves of heads. Measured with keys and values of 128 (other widths follow the same
+// lines: narrower values walk in fewer CTAs, narrower keys are not in the estimate), us, walk / bf16
+// chunks (f32 chunks):
+//   tokens x heads    32 x 16: 5.2 / 10.1 (13.7)   64 x 16: 8.9 / 9.8 (15.5)   128 x 16: 16.1 / 13.0 (25.6)
+//                     32 x 64: 10.0 / 10.7 (13.9)  32 x 256: 27 / 14.5 (27)   4 x 2048: 53 / 92 (178)
+//                     16 x 2048: 116 / 95 (186)
 // With offsets only the total is known here: one sequence may have all of it. Beyond 256 tokens
 // chunks are cut into units that run side by side.
 bool scan_is_quicker(const LinattnArgs& a, int type, bool few) {
@@ -242,7 +245,7 @@ bool scan_is_quicker(const LinattnArgs& a, int type, bool few) {
   const double scan = 2300 + 20 * heads * cols + (few ? 108 : 165) * longest + (crowd > 0 ? 2.6 * crowd * cols : 0);
   double chain, wave;
   if (type == MOE_F32) {
-    chain = 7500 + 8300 * chunks;
+    chain = 5200 + 10250 * chunks;
     wave = heads * (52 + 63 * chunks);
   } else if (type == MOE_F16) {
     chain = 7000 + 4000 * chunks;
