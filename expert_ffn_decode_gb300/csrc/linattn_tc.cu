@@ -16,8 +16,8 @@
 // Rounding: the tensor cores take 16-bit parts. A bf16 or f16 q, k, v is an operand as it is; f32
 // ones, and their scores, decayed keys and states as operands, are three bf16 parts, which are the
 // f32 value whatever its neighbours are. (Two f16 parts of the value times a power of two for the
-// tile are half the products, prefill of 2 x 1024 tokens 64 us, but values far below the tile's
-// largest lose their bits: a document before a reset took those of the one behind it.) For 16-bit types
+// tile are half the products, 2 x 1024 tokens x 16 heads 64 us against 68, but values far below the
+// tile's largest lose their bits: a document before a reset took those of the one behind it.) For 16-bit types
 // scores and the state as an operand keep two parts (16 bits in bf16, 22 in f16). The decayed keys
 // are summed into the f32 state, so they keep more bits for bf16 too: three bf16 parts or
 // two f16 ones. f16 parts need their values in f16's range: scores and states are scaled by a
