@@ -6,19 +6,21 @@
 //   S [rows][tokens] = Q K^T      O [rows][dim] += P V
 // with S, the weights P (over S, packed) and O in tensor memory, a row a lane. Its warps:
 //   0 .. 7, 8 .. 15    softmax of tile 0 and of tile 1, two threads a row: one tile's arithmetic beside the other's products
-//   16 .. 19, 20 .. 23  K's and V's codes to f16 operands in the 128-byte swizzle
+//   16 .. 19, 20 .. 23  K's codes to f16 operands, V's to bf16 ones, in the 128-byte swizzle
 //   24, 25             the warp that copies (codes, q), the one that issues products
 // K and V alternate through three places for codes and three for operands. Scales are powers of two and go into the
-// operands: K times 2^5 over the largest K scale of the 128 tokens, V times 2^5 over the largest V scale 2^E the CTA has
-// seen for the tiles, exact for scales down to 2^-29 of that (of e4m3's smallest codes to 2^-20) and 0 for smaller ones. A
-// thread then has three operations and an exponential for two scores. (Scales beside the operands, read from shared memory
-// for each score, took 505 us where this took 395: 512 tokens x 32 heads behind 32,768.) bf16 rows of q become f16 ones in
-// place, times a power of two a row: K in bf16 takes five operations a pair where f16 takes two (16,384-token prompt 2.93 ms
-// against 2.74).
-// Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 12 (powers of two; by 8,
-// with weights times 2^6, took 395 us where this took 376); then, and when E rises, the row of O is scaled in tensor
-// memory. Weights are made at once and kept back until no score was too large, else made again by code of their own. As
-// operands they are f16 times 2^3: 11 bits down to 2^-17 of the row's reference, fewer below.
+// operands: K times 2^5 over the largest K scale of the 128 tokens as f16, exact for scales down to 2^-29 of that (of e4m3's
+// smallest codes to 2^-20) and 0 for smaller ones, V as bf16 in units that depend on the largest V scale the CTA has seen for
+// the tiles: exact, whatever the others, while that one is below 2^25, and for scales down to 2^-140 of a larger one.
+// (Scales beside the operands, read from shared memory for each score, took 505 us where this took 395: 512 tokens x 32
+// heads behind 32,768.) bf16 rows of q become f16 ones in place, times a power of two a row.
+// Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 40 (powers of two); then,
+// and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
+// says whether the reference does, and for the weights, which are made over them.
+// As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
+// takes 2.74 ms for a 16,384-token prompt where this takes 3.39, but has 11 bits down to 2^-17 of the largest weight, fewer
+// below and none from 2^-28 on: behind a token that has 99.9% of the weight and next to no value, as trained models' first
+// tokens do, a 131,072-token row was 16% off.)
 //
 // No unit is full (counters of 512 tokens x 32 heads behind 32,768 tokens, 358 us: tensor pipe 36% of active cycles, issue
 // slots 46%, shared memory 31%): a tile's chain of products, weights and products is what a group's 5,500 cycles go into.
@@ -41,7 +43,10 @@ namespace {
 constexpr int TOK = 128;  // tokens of a group
 constexpr int SOFTMAX = 512, THREADS = SOFTMAX + 384;
 constexpr uint32_t HALF = 16384;  // 128 rows of 128 bytes: 64 dimensions of an operand of 128 rows
-constexpr float LIFT = 3.f, SLACK = 12.f;  // weights of up to 2^12 as f16 numbers of up to 2^15
+constexpr float SLACK = 40.f;  // weights of up to 2^40
+// V's operands are in units of 2^(unit - 127), unit a multiple of 16 that the largest scale byte is at most HEAD above: sums
+// of 2^30 weights of 2^SLACK times codes of 2^9 stay f32 numbers.
+constexpr int HEAD = 40;
 constexpr uint32_t T_S = 0, T_O = 256;  // tensor memory: 128 columns a tile each
 
 template <int DP>
@@ -66,18 +71,18 @@ struct alignas(16) Shared {
       p_ready[2], o_full[2];
   uint32_t tmem;
   int top[2][2][4];                // largest scale byte of a warp's tokens, K and V
-  int E[2];                        // of V for a group
+  int E[2];                        // of V for a group: what O is in units of
   float s_factor[2];               // of its scores
   alignas(16) uint32_t valid[2][2][4];  // tokens that count, as K's and V's warps found
   alignas(16) uint32_t nan[2][2][4];    // those of them with a NaN scale
-  uint32_t scale[2][2][TOK];       // what a token's codes are multiplied with, as a pair of operands; K and V
+  uint32_t scale[2][2][TOK];       // what a token's codes are multiplied with, as a pair of operands: K's f16, V's bf16
   float row[2][2][128];            // a row's two threads: their largest scores, their sums
 };
 
 static_assert(offsetof(Shared, valid) % 16 == 0 && offsetof(Shared, nan) % 16 == 0, "read sixteen bytes at a time");
 
-__device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {  // f16 operands
-  return 1u << 4 | (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 | 8u << 24;
+__device__ __forceinline__ uint32_t idesc(int n, bool bf16, bool b_mn) {  // operands f16 or bf16, both of them
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 | 8u << 24;
 }
 __device__ __forceinline__ uint64_t desc_sw128(const uint8_t* p, uint32_t lbo) {
   return (smem_desc(p, lbo, 1024) & ~((uint64_t)7 << 61)) | (uint64_t)2 << 61;
@@ -116,6 +121,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "%14, %15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
       "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int n>
@@ -157,9 +167,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Codes 2 hi, 2 hi + 1 of a word times a power of two (as a pair), in f16.
-template <int CODE>
+// Codes 2 hi, 2 hi + 1 of a word times a power of two (as a pair), in f16 or bf16.
+template <int CODE, bool BF16>
 __device__ __forceinline__ uint32_t scaled_pair(uint32_t w, bool hi, uint32_t f) {
+  if constexpr (BF16) {
+    if constexpr (CODE == MOE_I8) {  // as pair_of, times f: f (u - 256) - f / 2 max(u - 256, 0)
+      auto v = [](const uint32_t& x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+      const uint32_t u = __byte_perm(w, 0x43434343u, hi ? 0x4342 : 0x4140), one = 0x3f803f80u, off = 0xc380c380u, half = 0xbf00bf00u;
+      const __nv_bfloat162 twice = __hfma2_relu(v(u), v(one), v(off));
+      const __nv_bfloat162 z = __hfma2(twice, __hmul2(v(f), v(half)), __hfma2(v(u), v(f), __hmul2(v(f), v(off))));
+      return *reinterpret_cast<const uint32_t*>(&z);
+    }
+    const uint32_t x = pair_of<CODE, true>(w, hi);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&f));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
   const __half2 s = *reinterpret_cast<const __half2*>(&f);
   __half2 y;
   if constexpr (CODE == MOE_I8) {  // 1024 + 128 + code, less 1152, in one operation
@@ -171,10 +193,15 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t w, bool hi, uint32_t f)
   }
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
-  uint32_t p;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(hi), "f"(lo));
-  return p;
+// Two weights as two bf16 parts each.
+__device__ __forceinline__ void two_parts(float2 w, uint32_t& big, uint32_t& small) {
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(big) : "f"(w.y), "f"(w.x));
+  const float2 rest = fma2(make_float2(__uint_as_float(big << 16), __uint_as_float(big & 0xffff0000u)), make_float2(-1.f, -1.f), w);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(small) : "f"(rest.y), "f"(rest.x));
+}
+// 2^n for n up to 127, 0 below 2^-149.
+__device__ __forceinline__ float power_of(int n) {
+  return __uint_as_float(n >= -126 ? (uint32_t)(n + 127) << 23 : n >= -149 ? 1u << (n + 149) : 0u);
 }
 template <int threads>
 __device__ __forceinline__ bool all_of(int barrier, bool x) {  // whether x holds for all of some warps' threads
@@ -307,8 +334,8 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           uint32_t z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0;
-          tmem_st16(t_s, z);
-          tmem_st16(t_s + 16, z);
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) tmem_st16(t_s + c, z);
         } else {
           // which of 32 tokens from t0 + 64 part + 32 c on the row sees
           auto seen_of = [&](int c) {
@@ -319,48 +346,77 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           const float factor = sh.s_factor[par] * q_factor;
           const int E1 = sh.E[par];
           bool stays;
-          // ---- weights by the row's reference as it is, kept back until it is known to do ----
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // ---- the scores by the row's reference as it is: weights if it does ----
           float top[2] = {-INFINITY, -INFINITY};
           {
-            uint32_t p[32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x[32];
+            auto scores = [&](int c, float (&x)[32]) {  // of 32 tokens, by the row's reference
               tmem_ld32(t_s + c * 32, x);
               tmem_ld_wait();
-              float2 f2 = make_float2(factor, factor), ref = make_float2(LIFT - m, LIFT - m);
+              float2 f2 = make_float2(factor, factor), ref = make_float2(-m, -m);
               if (!whole) {
                 const uint32_t seen = seen_of(c), bad = sh.nan[0][par][part * 2 + c] | sh.nan[1][par][part * 2 + c];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  x[i] = seen >> i & 1 ? fmaf(x[i], factor, ref.x) : -INFINITY;
+                  x[i] = seen >> i & 1 ? fmaf(x[i], factor, -m) : -INFINITY;
                   if (seen & bad & 1u << i) x[i] = __uint_as_float(0x7fc00000u);
                 }
                 f2 = make_float2(1.f, 1.f), ref = make_float2(0.f, 0.f);
               }
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float2 d0 = fma2(make_float2(x[i], x[i + 1]), f2, ref), d1 = fma2(make_float2(x[i + 2], x[i + 3]), f2, ref);
-                top[0] = max3(top[0], d0.x, d0.y);
-                top[1] = max3(top[1], d1.x, d1.y);
-                const float2 w0 = make_float2(ex2(d0.x), ex2(d0.y)), w1 = make_float2(ex2(d1.x), ex2(d1.y));
-                sum[0] = add2(sum[0], w0);
-                sum[1] = add2(sum[1], w1);
-                p[c * 16 + i / 2] = half_pair(w0.x, w0.y);
-                p[c * 16 + i / 2 + 1] = half_pair(w1.x, w1.y);
+              for (int i = 0; i < 32; i += 2) {
+                const float2 d = fma2(make_float2(x[i], x[i + 1]), f2, ref);
+                x[i] = d.x, x[i + 1] = d.y;
               }
+            };
+            if (whole) {  // (factors are not negative)
+              float x[32], y[32];
+              tmem_ld32(t_s, x);
+              tmem_ld32(t_s + 32, y);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                top[0] = max3(top[0], x[i], x[i + 1]);
+                top[1] = max3(top[1], y[i], y[i + 1]);
+              }
+              top[0] = fmaf(fmaxf(top[0], top[1]), factor, -m);
+            } else {
+#pragma unroll 1
+              for (int c = 1; c >= 0; --c) {
+                float x[32];
+                scores(c, x);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  top[0] = max3(top[0], x[i], x[i + 1]);
+                  top[1] = max3(top[1], x[i + 2], x[i + 3]);
+                }
+              }
+              top[0] = fmaxf(top[0], top[1]);
             }
-            const float mx = fmaxf(top[0], top[1]) - LIFT;
-            const bool need = real && (fresh ? mx > -INFINITY : mx > SLACK);
+            const bool need = real && (fresh ? top[0] > -INFINITY : top[0] > SLACK);
             stays = all_of<64>(pair, !need && E1 == E);
             if (stays) {
-              tmem_st16(t_s, p);
-              tmem_st16(t_s + 16, p + 16);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                float x[32];
+                scores(c, x);
+#pragma unroll
+                for (int y = 0; y < 32; y += 16) {
+                  uint32_t big[8], small[8];
+#pragma unroll
+                  for (int i = 0; i < 16; i += 4) {
+                    const float2 w0 = make_float2(ex2(x[y + i]), ex2(x[y + i + 1])), w1 = make_float2(ex2(x[y + i + 2]), ex2(x[y + i + 3]));
+                    sum[0] = add2(sum[0], w0);
+                    sum[1] = add2(sum[1], w1);
+                    two_parts(w0, big[i / 2], small[i / 2]);
+                    two_parts(w1, big[i / 2 + 1], small[i / 2 + 1]);
+                  }
+                  tmem_st8(t_s + c * 32 + y / 2, big);
+                  tmem_st8(t_s + c * 32 + 16 + y / 2, small);
+                }
+              }
               const float2 both = add2(sum[0], sum[1]);
               l += both.x + both.y;
-            } else {
-              top[0] = mx;
             }
           }
           if (!stays) {
@@ -392,19 +448,20 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
             for (int c = 0; c < 2; ++c) {
               const uint32_t seen = seen_of(c), bad = sh.nan[0][par][part * 2 + c] | sh.nan[1][par][part * 2 + c];
               float x[32];
-              uint32_t p[16];
+              uint32_t big[16], small[16];
               tmem_ld32(t_s + c * 32, x);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 // (scores of 2^27 and more have steps beyond the slack: their references are not exact)
-                x[i] = seen >> i & 1 ? ex2(fminf(fmaf(x[i], factor, LIFT - m), LIFT + SLACK)) : 0.f;
+                x[i] = seen >> i & 1 ? ex2(fminf(fmaf(x[i], factor, -m), SLACK)) : 0.f;
                 if (seen & bad & 1u << i) x[i] = __uint_as_float(0x7fc00000u);
                 more += x[i];
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) p[i] = half_pair(x[2 * i], x[2 * i + 1]);
-              tmem_st16(t_s + c * 16, p);  // (over scores that have been read)
+              for (int i = 0; i < 16; ++i) two_parts(make_float2(x[2 * i], x[2 * i + 1]), big[i], small[i]);
+              tmem_st16(t_s + c * 32, big);  // (over scores that have been read)
+              tmem_st16(t_s + c * 32 + 16, small);
             }
             l += more;
           }
@@ -413,7 +470,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         tc_fence_before_sync();
         mbar_arrive(&sh.p_ready[h]);
       }
-      // ---- the piece's rows: sums in units of 2^(m - LIFT), o of 2^(E - 5) times that ----
+      // ---- the piece's rows: sums in units of 2^m, o of 2^E times that ----
       if (n_groups > 0) {
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.o_full[h], filled & 1));
         tc_fence_after_sync();
@@ -421,8 +478,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       }
       sh.row[h][part][r] = l;
       pair_sync();
-      l = (l + sh.row[h][part ^ 1][r]) * (1.f / 8.f);
-      E -= 5 + (int)LIFT;
+      l += sh.row[h][part ^ 1][r];
       const bool nothing = fresh && l == 0.f;
       const bool own = pc.c0 == pc.c1;
       const int64_t at = (int64_t)(cta == pc.c0 ? pc.slot0 : 2 * cta) * f.rows + h * half_rows + r;
@@ -467,7 +523,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
     // ---- codes to operands: K's warps, which see to the scales as well, and V's --------------------------------
     fewer_registers<40>();
     const int which = warp >= SOFTMAX / 32 + 4, ct = tid & 127;
-    const float scale2 = a.scale * 1.44269504f;
+    const float scale2 = fabsf(a.scale) * 1.44269504f;
     const int nb = 1 << (a.page_log - a.block_log), page_mask = (1 << a.page_log) - 1;
     uint32_t group = 0;
     for (int k = 0;; ++k) {
@@ -509,14 +565,15 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         for (int w = 0; w < 4; ++w) top = max(top, sh.top[which][par][w]);
         {
           const bool live = page >= 0 && byte < 255;
-          uint32_t scale;  // 2^(byte - top + 5), 0 from 2^-25 on
-          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(__uint_as_float((uint32_t)max(132 + byte - top, 1) << 23)));
+          const int unit = max(0, (top - HEAD + 15) & ~15);
+          uint32_t scale;  // K: 2^(byte - top + 5), 0 from 2^-25 on; V: 2^(byte - unit)
+          if (which) asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(power_of(byte - unit)));
+          else asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(__uint_as_float((uint32_t)max(132 + byte - top, 1) << 23)));
+          if (!which && a.scale < 0.f) scale ^= 0x80008000u;  // (so that the scores' factors are not negative)
           sh.scale[which][par][ct] = live ? scale : 0u;
+          if (which && ct == 0) sh.E[par] = unit - 127;
         }
-        if (ct == 0) {
-          if (which) sh.E[par] = top - 127;
-          else sh.s_factor[par] = ldexpf(scale2, top - 127 - 5);
-        }
+        if (!which && ct == 0) sh.s_factor[par] = ldexpf(scale2, top - 127 - 5);
         all_of<128>(2 + which, true);  // the scales are there
         // 16 codes a turn; eight neighbouring lanes take four pieces of two tokens, which the swizzle (16-byte pieces
         // exchanged by the row's number) puts into different banks
@@ -526,20 +583,24 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         uint8_t* dst = sm + P::OPS + slot * P::OPERAND + (c / 4) * HALF + t1 * 128;
         if (c * 16 < D) {
           const uint32_t* sc = sh.scale[which][par] + t1;
+          auto convert = [&](auto bf16) {
 #pragma unroll
-          for (int i = 0; i < TOK / TURN; ++i) {
-            const int t = t1 + i * TURN;
-            const uint4 u = *reinterpret_cast<const uint4*>(src + i * TURN * D);
-            const uint32_t f = sc[i * TURN];
-            const uint32_t w[4] = {code_word<CODE>(u.x), code_word<CODE>(u.y), code_word<CODE>(u.z), code_word<CODE>(u.w)};
-            uint32_t x[8];
+            for (int i = 0; i < TOK / TURN; ++i) {
+              const int t = t1 + i * TURN;
+              const uint4 u = *reinterpret_cast<const uint4*>(src + i * TURN * D);
+              const uint32_t f = sc[i * TURN];
+              const uint32_t w[4] = {code_word<CODE>(u.x), code_word<CODE>(u.y), code_word<CODE>(u.z), code_word<CODE>(u.w)};
+              uint32_t x[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) x[y] = scaled_pair<CODE>(w[y / 2], y & 1, f);
-            uint8_t* row = dst + i * TURN * 128;
-            const int at = ((2 * c) & 7) ^ (t & 7);
-            *reinterpret_cast<uint4*>(row + (at << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(row + ((at ^ 1) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-          }
+              for (int y = 0; y < 8; ++y) x[y] = scaled_pair<CODE, decltype(bf16)::value>(w[y / 2], y & 1, f);
+              uint8_t* row = dst + i * TURN * 128;
+              const int at = ((2 * c) & 7) ^ (t & 7);
+              *reinterpret_cast<uint4*>(row + (at << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(row + ((at ^ 1) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          };
+          if (which) convert(std::true_type{});
+          else convert(std::false_type{});
           if (CODE == MOE_E4M3 && which) {  // what does not count may be no numbers, and would not go with weights of 0
             const uint4 v = *reinterpret_cast<const uint4*>(sh.valid[1][par]);
             if ((v.x & v.y & v.z & v.w) != ~0u)
@@ -660,7 +721,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       // ---- products -----------------------------------------------------------------------------------------
       if (elect_one()) {
         const int steps = D / 16;
-        const uint32_t s_desc = idesc(TOK, false), o_desc = idesc(D, true);
+        const uint32_t s_desc = idesc(TOK, false, false), o_desc = idesc(D, true, true);
         uint32_t unit = 0, group = 0, filled = 0;
         auto op_ready = [&](uint32_t u) { ok = ok && mbar_wait(&sh.op_full[u % 3], u / 3 & 1); };
         const uint64_t q_desc = desc_sw128(sm + P::Q, 16), k_desc = desc_sw128(sm + P::OPS, 16), v_desc = desc_sw128(sm + P::OPS, HALF);
@@ -677,7 +738,10 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           const uint32_t v = (uint32_t)v_desc + u % 3 * (P::OPERAND >> 4);
 #pragma unroll
           for (int s = 0; s < TOK / 16; ++s)
-            mma_ts(tm + T_O + h * 128, tm + T_S + h * 128 + s / 4 * 64 + s % 4 * 8, v + (s * 2048 >> 4), hi, o_desc, !first || s > 0);
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+              mma_ts(tm + T_O + h * 128, tm + T_S + h * 128 + s / 2 * 32 + p * 16 + s % 2 * 8, v + (s * 2048 >> 4), hi, o_desc,
+                     !first || s > 0 || p == 0);
         };
         for (int k = 0; ok; ++k) {
           ok = mbar_wait(&sh.piece_full[k & 1], k >> 1 & 1);
