@@ -16,9 +16,10 @@
 //
 // Operands: codes are exact in f16 and bf16. f16 rows are operands as they are; bf16 rows are f16 times a power
 // of two a row (as they are down to 2^-32 of the row's largest); f32 ones are three bf16 parts, which are the
-// value. Weights are f16 times 2^6, one part for bf16 outputs (11 bits) and two for f16 ones (22), down to 2^-20 of
-// the row's largest product of weight and V scale and fewer bits below (bf16 weights would keep theirs, and V's
-// codes as bf16 take five instructions a pair where f16 takes two); for f32 they are three bf16 parts.
+// value. Weights are bf16 parts, whose bits go by each weight's own size: two for bf16 outputs (16 bits), three for the
+// others (24). (f16 parts, one or two, on V's codes in f16, which take two instructions a pair where bf16 takes four, lost
+// bits below 2^-20 of the row's largest product of weight and V scale and all below 2^-30: 64 sequences 211 us where this
+// takes 217, but 3,000 tokens behind a first one of 2^27 times each one's weight and no value were 1.5% off, of 2^45 lost.)
 //
 // The call's groups of tokens, of all sequences, row tiles and heads, are one line that the CTAs cut into
 // equal pieces, two CTAs an SM. A tile and head that a cut goes through is joined by the CTA that is done with its part last,
@@ -121,10 +122,9 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
   using P = FewPlan<T, DP, NT>;
   constexpr bool F32 = std::is_same<T, float>::value, BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr int WARPS = P::WARPS, THREADS = 32 * WARPS, U = P::U, GROUP = P::GROUP;
-  constexpr int QP = F32 ? 3 : 1, PP = F32 ? 3 : BF ? 1 : 2;  // parts of q and of the weights
+  constexpr int QP = F32 ? 3 : 1, PP = BF ? 2 : 3;  // parts of q and of the weights
   constexpr int KJ = DP / 64, VJ = DP == 256 ? 2 : 1, MT = DP / 16;
-  // weights up to 2^8, as f16 operands up to 2^14
-  constexpr float LIFT = F32 ? 0.f : 6.f, MOST1 = F32 ? 1.f : 64.f, MOSTV = 256.f * MOST1;
+  constexpr float MOST = 256.f;  // weights up to 2^8
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ FewShared<WARPS, GROUP> sh;
@@ -453,10 +453,10 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
             for (int e = 0; e < 4; ++e) {
               const float d = sc[u][n][e] - m[n][e & 1];
               w1[u][n][e] = ex2(d);
-              wv[u][n][e] = ex2(d + (ev[u][e >> 1] - (E[n][e & 1] - LIFT)));
-              top = fmaxf(top, fmaxf(w1[u][n][e] * MOST1, wv[u][n][e]));
+              wv[u][n][e] = ex2(d + (ev[u][e >> 1] - E[n][e & 1]));
+              top = fmaxf(top, fmaxf(w1[u][n][e], wv[u][n][e]));
             }
-        return top > MOSTV;
+        return top > MOST;
       };
       if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
@@ -503,17 +503,17 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
               if (!whole && sc[u][n][2 * e + c2] == -INFINITY) wv[u][n][2 * e + c2] = 0.f;  // (a NaN scale behind the mask)
             }
             uint32_t h[PP];
-            split_pair<PP, F32>(wv[u][n][2 * e], wv[u][n][2 * e + 1], h);
+            split_pair<PP, true>(wv[u][n][2 * e], wv[u][n][2 * e + 1], h);
 #pragma unroll
             for (int k = 0; k < PP; ++k) pf[k][n][e] = transpose8(h[k]);
           }
         auto value_tile = [&](int i, uint32_t lo, uint32_t hi) {  // words of tokens (2 qt, + 1) and (2 qt + 8, + 9)
-          const uint32_t A[4] = {pair_of<CODE, F32>(lo, false), pair_of<CODE, F32>(lo, true), pair_of<CODE, F32>(hi, false),
-                                 pair_of<CODE, F32>(hi, true)};
+          const uint32_t A[4] = {pair_of<CODE, true>(lo, false), pair_of<CODE, true>(lo, true), pair_of<CODE, true>(hi, false),
+                                 pair_of<CODE, true>(hi, true)};
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = PP - 1; k >= 0; --k) mma<F32>(o[i][n], A, pf[k][n]);
+            for (int k = PP - 1; k >= 0; --k) mma<true>(o[i][n], A, pf[k][n]);
         };
 #pragma unroll
         for (int j = 0; j < VJ; ++j) {
@@ -586,7 +586,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         }
         const float E1 = M == LOWEST ? 0.f : ceilf(top);
         keep[n][c2] = ex2((m[n][c2] - M) + (E[n][c2] - E1));
-        all[n][c2] = Stats{M, E1 - LIFT, L, 0.f};
+        all[n][c2] = Stats{M, E1, L, 0.f};
       }
     const bool own = pc.c0 == pc.c1;
     const int64_t part = (int64_t)(cta == pc.c0 ? pc.slot0 : 2 * cta) * f.rows;

@@ -19,8 +19,8 @@
 // says whether the reference does, and for the weights, which are made over them.
 // As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
 // takes 2.74 ms for a 16,384-token prompt where this takes 3.39, but has 11 bits down to 2^-17 of the largest weight, fewer
-// below and none from 2^-28 on: behind a token that has 99.9% of the weight and next to no value, as trained models' first
-// tokens do, a 131,072-token row was 16% off.)
+// below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
+// value, as in trained models.)
 //
 // No unit is full (counters of 512 tokens x 32 heads behind 32,768 tokens, 358 us: tensor pipe 36% of active cycles, issue
 // slots 46%, shared memory 31%): a tile's chain of products, weights and products is what a group's 5,500 cycles go into.

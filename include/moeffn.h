@@ -465,10 +465,10 @@ int moe_kv8_read(const void* cache, const int32_t* offsets, const int32_t* past,
  * The sinks [n_heads] f32 are logits that take weight and add no value (NULL: none; flint_moe_ssd.js,
  * SOFTMAX_SINK). A row that sees nothing becomes 0. `workspace` as for moe_ffn_forward_ex, of at
  * least moe_kv8_workspace_size(cfg) bytes.
- * Bits: scores, softmax statistics and sums are f32, o is rounded once. As operands the weights of sequences of more than
- * 48 rows (tokens x heads that share a key/value head) of 16-bit types and heads of up to 128 have 16 bits each, whatever
- * their sizes, and V is exact while no scale among the tile's tokens is above 2^25 (else for scales down to 2^-140 of the
- * largest). (Scores beyond f32's range are infinities
+ * Bits: scores, softmax statistics and sums are f32, o is rounded once. As operands the weights have 16 bits (bf16, and
+ * f16 sequences of more than 48 rows: tokens x heads that share a key/value head) or 24 (the others), each by its own size,
+ * however small it is beside the row's largest. V is exact; in sequences of more than 48 rows of 16-bit types and heads of up
+ * to 128 while no V scale among a tile's tokens is above 2^25, else for scales down to 2^-140 of the largest. (Scores beyond f32's range are infinities
  * and what their rows become is open.) A row of q that holds an infinity or a
  * NaN gives a row that is not finite, and so does a NaN block that a row sees; neither reaches other
  * rows. */
