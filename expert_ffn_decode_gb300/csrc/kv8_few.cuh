@@ -158,7 +158,6 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
     // ---- the warp that fetches: pieces, their rows of q, and a group for every warp in turn -------------
     const int page_mask = (1 << a.page_log) - 1, nb = 1 << (a.page_log - a.block_log);
     const int page_rows = (int)(a.page_bytes >> 7), head_rows = a.D << a.page_log >> 7;  // of 128 bytes
-    const float scale2 = a.scale * 1.44269504f;
     const uint64_t policy = policy_evict_first();
     int b = b0;
     Seq s = seq_of<GROUP>(a, b, f.rows);
@@ -267,8 +266,8 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-          // factors of the scores (a scale of 2^-127 counts as 0), exponents of the values
-          auto k_of = [&](int x) { return x == 255 ? nan : __uint_as_float((uint32_t)x << 23) * scale2; };
+          // factors of the scores (kv8_power, in the fewest operations: all warps wait for this one), exponents of the values
+          auto k_of = [&](int x) { return x == 255 ? nan : __uint_as_float(max((uint32_t)x << 23, 0x400000u)); };
           auto v_of = [&](int x) { return x == 255 ? nan : (float)(x - 127); };
           if constexpr (U == 1) {
             if (lane < 16) sh.k_factor[w][st][lane] = k_of(sc[w][0]);
@@ -327,7 +326,9 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
 
     // ---- q ----
     uint32_t qf[QP][NT][KJ * 4][2];
-    float rf[NT][2];
+    // A score is its sum times a factor of the row, K's scale and another factor of the row: no product of three of them
+    // leaves f32 on its way to a score that does not.
+    float rf[NT][2], rf2[NT][2];
     int pos[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -350,7 +351,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
           }
         }
       float mul = 1.f, inv = 1.f;
-      if constexpr (BF) {  // the row's largest to 2^14 .. 2^15
+      if constexpr (BF || F32) {  // the row's largest to 2^14 .. 2^15
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(max((int)(__float_as_uint(top) >> 23), 16), 254);
@@ -370,7 +371,9 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        rf[n][c] = __shfl_sync(0xffffffffu, inv, (2 * qt + c) * 4);
+        const float factor = __shfl_sync(0xffffffffu, inv, (2 * qt + c) * 4);
+        rf[n][c] = factor > 1.f ? 1.f : factor;
+        rf2[n][c] = fminf(fmaxf(fmaxf(factor, 1.f) * a.scale * 1.44269504f, -3e38f), 3e38f);
         pos[n][c] = pc.past + (row0 + 8 * n + 2 * qt + c) / a.rep;
       }
     }
@@ -428,7 +431,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
           for (int e = 0; e < 4; ++e) {
             float x = S[0][n][e] + S[1][n][e];
             if constexpr (SN == 4) x += S[2][n][e] + S[3][n][e];
-            sc[u][n][e] = x * rf[n][e & 1] * kf[e >> 1];
+            sc[u][n][e] = x * rf[n][e & 1] * kf[e >> 1] * rf2[n][e & 1];
           }
       }
       if (!whole) {

@@ -18,7 +18,7 @@
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
 // As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
-// takes 2.74 ms for a 16,384-token prompt where this takes 3.39, but has 11 bits down to 2^-17 of the largest weight, fewer
+// takes 2.74 ms for a 16,384-token prompt where this takes 3.23, but has 11 bits down to 2^-17 of the largest weight, fewer
 // below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
 // value, as in trained models.)
 //
@@ -72,7 +72,7 @@ struct alignas(16) Shared {
   uint32_t tmem;
   int top[2][2][4];                // largest scale byte of a warp's tokens, K and V
   int E[2];                        // of V for a group: what O is in units of
-  float s_factor[2];               // of its scores
+  int s_exp[2];                    // its scores are sums times 2^s_exp
   alignas(16) uint32_t valid[2][2][4];  // tokens that count, as K's and V's warps found
   alignas(16) uint32_t nan[2][2][4];    // those of them with a NaN scale
   uint32_t scale[2][2][TOK];       // what a token's codes are multiplied with, as a pair of operands: K's f16, V's bf16
@@ -203,6 +203,12 @@ __device__ __forceinline__ void two_parts(float2 w, uint32_t& big, uint32_t& sma
 __device__ __forceinline__ float power_of(int n) {
   return __uint_as_float(n >= -126 ? (uint32_t)(n + 127) << 23 : n >= -149 ? 1u << (n + 149) : 0u);
 }
+// scale * 2^n, the exponents of q and K added up first: neither's power alone need be an f32 number. (Sums below 2^35 make
+// scores of no more than 2^-90 with what is 0 here; from 2^120 on scores are not told apart.)
+__device__ __forceinline__ float score_factor(float scale, int n) {
+  n = max(min(n, 120), -250);
+  return __uint_as_float((uint32_t)((n >> 1) + 127) << 23) * scale * __uint_as_float((uint32_t)(n - (n >> 1) + 127) << 23);
+}
 template <int threads>
 __device__ __forceinline__ bool all_of(int barrier, bool x) {  // whether x holds for all of some warps' threads
   uint32_t r;
@@ -263,6 +269,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
     const uint32_t lanes = tm + ((uint32_t)(warp & 3) * 32u << 16);
     const uint32_t t_s = lanes + T_S + h * 128 + part * 64, t_o = lanes + T_O + h * 128;  // weights: over the first half of t_s
     const int window = a.window ? a.window : 1 << 30;
+    const float scale2 = fabsf(a.scale) * 1.44269504f;
     uint32_t group = 0, filled = 0;          // groups and pieces with some so far
     auto rows_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(SOFTMAX) : "memory"); };
     const int pair = 4 + h * 4 + (warp & 3);  // the barrier of the two warps that share rows
@@ -277,7 +284,8 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       const int t_last = first + half_tokens - 1;  // of the tile's last row
       const bool real = r < half_rows && pc.row0 + h * half_rows + r < pc.n * a.rep;
       const bool tile_real = pc.row0 + h * half_rows < pc.n * a.rep;
-      float m = 0.f, l = 0.f, q_factor = 1.f;
+      float m = 0.f, l = 0.f;
+      int q_exp = 0;  // rows of q are their operands times 2^q_exp
       bool fresh = true;  // has seen no token
       int E = 0;
       const int n_groups = pc.g1 - pc.g0;
@@ -303,7 +311,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           pair_sync();
           const int e = min(max((int)(max(most, __float_as_uint(sh.row[h][part ^ 1][r])) >> 7), 16), 254);
           const float mul = __uint_as_float((uint32_t)(268 - e) << 23);
-          q_factor = __uint_as_float((uint32_t)(e - 14) << 23);
+          q_exp = e - 141;
           if (real && ok) {
 #pragma unroll 1
             for (int c = part; c < DP / 8; c += 2) {
@@ -343,7 +351,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
             const int lo = min(max(max(pos - window + 1, 0) - tc, 0), 32), hi = min(max(pos + 1 - tc, 0), 32);
             return sh.valid[0][par][part * 2 + c] & (uint32_t)((1ull << hi) - (1ull << min(lo, hi)));
           };
-          const float factor = sh.s_factor[par] * q_factor;
+          const float factor = score_factor(scale2, sh.s_exp[par] + q_exp);
           const int E1 = sh.E[par];
           bool stays;
           // ---- the scores by the row's reference as it is: weights if it does ----
@@ -523,7 +531,6 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
     // ---- codes to operands: K's warps, which see to the scales as well, and V's --------------------------------
     fewer_registers<40>();
     const int which = warp >= SOFTMAX / 32 + 4, ct = tid & 127;
-    const float scale2 = fabsf(a.scale) * 1.44269504f;
     const int nb = 1 << (a.page_log - a.block_log), page_mask = (1 << a.page_log) - 1;
     uint32_t group = 0;
     for (int k = 0;; ++k) {
@@ -573,7 +580,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           sh.scale[which][par][ct] = live ? scale : 0u;
           if (which && ct == 0) sh.E[par] = unit - 127;
         }
-        if (!which && ct == 0) sh.s_factor[par] = ldexpf(scale2, top - 127 - 5);
+        if (!which && ct == 0) sh.s_exp[par] = top - 127 - 5;
         all_of<128>(2 + which, true);  // the scales are there
         // 16 codes a turn; eight neighbouring lanes take four pieces of two tokens, which the swizzle (16-byte pieces
         // exchanged by the row's number) puts into different banks

@@ -1,0 +1,48 @@
+"""Attention over the 8-bit cache at the ends of its numbers: rows of q and keys whose sizes are far from 1 and whose
+scores are not, scales of 2^-127. Bounds: tests/kv8_bounds.py."""
+
+import numpy as np
+import pytest
+
+from tests.kv8_bounds import check
+from tests.kv8_cases import Cache, types
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+TYPES = ["bf16", "f16", "f32"]
+
+
+def keys_at(c, byte):
+    """All scales of K, with a spread of a few powers of two."""
+    for g in range(c.G):
+        for p in range(c.n_pages):
+            s = c.scales_of(c.cache, p, g, 0)
+            s[:] = np.clip(byte + c.rng.integers(-1, 2, s.shape), 0, 254)
+
+
+@pytest.mark.parametrize("type,power", [("bf16", 100), ("bf16", 121), ("f32", 100), ("f32", 121), ("bf16", -100), ("f32", -100),
+                                        ("bf16", -120), ("f32", -120), ("f16", 12), ("f16", -12)])
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("step", [True, False])
+def test_factors_far_from_1(type, power, code, step):
+    """q of 2^power, K of about 2^-power (from scale bytes of 0 on): scores of a few units, as for sizes around 1."""
+    c = Cache([(300, 1), (40, 1)] if step else [(200, 90), (0, 70)], D=64, type=type, code=code, seed=41)
+    keys_at(c, (121 if code == "i8" else 120) - power)
+    c.upload()
+    q, _ = c.rows(c.H * c.D, 2.0 ** power)
+    check(c, c.attend(q, step=step), q.double().cpu().numpy(), rows=11)
+
+
+@pytest.mark.parametrize("type", ["bf16", "f32"])
+@pytest.mark.parametrize("step", [True, False])
+def test_a_scale_of_0_is_no_zero(type, step):
+    """Byte 0 stands for 2^-127 in K as well."""
+    c = Cache([(200, 1)] if step else [(100, 80)], D=64, type=type, seed=42)
+    for g in range(c.G):
+        for p in range(c.n_pages):
+            c.scales_of(c.cache, p, g, 0)[:] = 0
+    c.upload()
+    q, _ = c.rows(c.H * c.D, 2.0 ** 119)
+    o = c.attend(q, step=step)
+    check(c, o, q.double().cpu().numpy(), rows=11)
+    assert not torch.equal(o, c.attend(q * 0, step=step))
