@@ -10,7 +10,7 @@
 //   24, 25             the warp that copies (codes, q), the one that issues products
 // K and V alternate through three places for codes and three for operands. Scales are powers of two and go into the
 // operands: K times 2^5 over the largest K scale of the 128 tokens as f16, exact for scales down to 2^-29 of that (of e4m3's
-// smallest codes to 2^-20) and 0 for smaller ones, V as bf16 in units that depend on the largest V scale the CTA has seen for
+// smallest codes to 2^-20; where one is smaller, no scale of the group goes in, and scores get theirs one by one), V as bf16 in units that depend on the largest V scale the CTA has seen for
 // the tiles: exact, whatever the others, while that one is below 2^25, and for scales down to 2^-140 of a larger one.
 // (Scales beside the operands, read from shared memory for each score, took 505 us where this took 395: 512 tokens x 32
 // heads behind 32,768.) bf16 rows of q become f16 ones in place, times a power of two a row.
@@ -18,7 +18,7 @@
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
 // As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
-// takes 2.74 ms for a 16,384-token prompt where this takes 3.23, but has 11 bits down to 2^-17 of the largest weight, fewer
+// takes 2.74 ms for a 16,384-token prompt where this takes 3.31, but has 11 bits down to 2^-17 of the largest weight, fewer
 // below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
 // value, as in trained models.)
 //
@@ -47,6 +47,7 @@ constexpr float SLACK = 40.f;  // weights of up to 2^40
 // V's operands are in units of 2^(unit - 127), unit a multiple of 16 that the largest scale byte is at most HEAD above: sums
 // of 2^30 weights of 2^SLACK times codes of 2^9 stay f32 numbers.
 constexpr int HEAD = 40;
+constexpr int FAR = 1 << 20;
 constexpr uint32_t T_S = 0, T_O = 256;  // tensor memory: 128 columns a tile each
 
 template <int DP>
@@ -70,9 +71,10 @@ struct alignas(16) Shared {
   uint64_t piece_full[2], piece_free[2], q_full, q_ready, q_free, raw_full[3], raw_free[3], op_full[3], op_free[3], s_full[2],
       p_ready[2], o_full[2];
   uint32_t tmem;
-  int top[2][2][4];                // largest scale byte of a warp's tokens, K and V
+  int top[2][2][4], low[2][4];     // largest scale byte of a warp's tokens, K and V, smallest of K
   int E[2];                        // of V for a group: what O is in units of
-  int s_exp[2];                    // its scores are sums times 2^s_exp
+  int s_exp[2];                    // its scores are sums times 2^s_exp; where K's scales are too far apart for that, FAR
+  alignas(4) uint8_t k_byte[2][TOK];  // and each token's times its own scale
   alignas(16) uint32_t valid[2][2][4];  // tokens that count, as K's and V's warps found
   alignas(16) uint32_t nan[2][2][4];    // those of them with a NaN scale
   uint32_t scale[2][2][TOK];       // what a token's codes are multiplied with, as a pair of operands: K's f16, V's bf16
@@ -337,7 +339,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         const uint4 valid = *reinterpret_cast<const uint4*>(sh.valid[0][par]);
         const uint4 nk = *reinterpret_cast<const uint4*>(sh.nan[0][par]), nv = *reinterpret_cast<const uint4*>(sh.nan[1][par]);
         const bool whole = (valid.x & valid.y & valid.z & valid.w) == ~0u && t0 + TOK - 1 <= first && t0 > t_last - window &&
-                           (nk.x | nk.y | nk.z | nk.w | nv.x | nv.y | nv.z | nv.w) == 0;
+                           sh.s_exp[par] != FAR && (nk.x | nk.y | nk.z | nk.w | nv.x | nv.y | nv.z | nv.w) == 0;
         if (!tile_real || t0 > t_last || t0 + TOK - 1 <= first - window) {  // the mask leaves the tile's rows nothing here
           uint32_t z[16];
 #pragma unroll
@@ -351,7 +353,20 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
             const int lo = min(max(max(pos - window + 1, 0) - tc, 0), 32), hi = min(max(pos + 1 - tc, 0), 32);
             return sh.valid[0][par][part * 2 + c] & (uint32_t)((1ull << hi) - (1ull << min(lo, hi)));
           };
-          const float factor = score_factor(scale2, sh.s_exp[par] + q_exp);
+          const bool far = sh.s_exp[par] == FAR;  // (for all tokens of the group)
+          const float factor = far ? 1.f : score_factor(scale2, sh.s_exp[par] + q_exp);
+          auto factors = [&](int c, float* x) {  // scores of 32 tokens from sums that their scales are not in yet
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const uint32_t bytes = *reinterpret_cast<const uint32_t*>(&sh.k_byte[par][part * 64 + c * 32 + i]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int n = max(min((int)(bytes >> 8 * y & 255) - 127 + q_exp, 120), -250);
+                x[i + y] *= __uint_as_float((uint32_t)((n >> 1) + 127) << 23);
+                x[i + y] *= scale2 * __uint_as_float((uint32_t)(n - (n >> 1) + 127) << 23);
+              }
+            }
+          };
           const int E1 = sh.E[par];
           bool stays;
           // ---- the scores by the row's reference as it is: weights if it does ----
@@ -362,6 +377,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
               tmem_ld_wait();
               float2 f2 = make_float2(factor, factor), ref = make_float2(-m, -m);
               if (!whole) {
+                if (far) factors(c, x);
                 const uint32_t seen = seen_of(c), bad = sh.nan[0][par][part * 2 + c] | sh.nan[1][par][part * 2 + c];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -459,6 +475,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
               uint32_t big[16], small[16];
               tmem_ld32(t_s + c * 32, x);
               tmem_ld_wait();
+              if (far) factors(c, x);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 // (scores of 2^27 and more have steps beyond the slack: their references are not exact)
@@ -559,6 +576,11 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         if (unit >= 3) ok = ok && mbar_wait(&sh.op_free[slot], unit / 3 - 1 & 1);
         const uint32_t valid = __ballot_sync(0xffffffffu, page >= 0), nan = __ballot_sync(0xffffffffu, page >= 0 && byte == 255);
         const int most = __reduce_max_sync(0xffffffffu, page >= 0 && byte < 255 ? byte : 0);
+        if (which == 0) {
+          const int least = __reduce_min_sync(0xffffffffu, page >= 0 && byte < 255 ? byte : 255);
+          if (lane == 0) sh.low[par][warp & 3] = least;
+          sh.k_byte[par][ct] = (uint8_t)byte;
+        }
         if (lane == 0) {
           sh.valid[which][par][warp & 3] = valid;
           sh.nan[which][par][warp & 3] = nan;
@@ -573,14 +595,24 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         {
           const bool live = page >= 0 && byte < 255;
           const int unit = max(0, (top - HEAD + 15) & ~15);
-          uint32_t scale;  // K: 2^(byte - top + 5), 0 from 2^-25 on; V: 2^(byte - unit)
+          // K's codes as f16 have their bits down to 2^-24: scales that differ by more do not go into one operand
+          bool far = false;
+          if (!which) {
+            int low = 255;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) low = min(low, sh.low[par][w]);
+            far = top - low > (CODE == MOE_I8 ? 29 : 20);
+          }
+          uint32_t scale;  // K: 2^(byte - top + 5); V: 2^(byte - unit)
           if (which) asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(power_of(byte - unit)));
-          else asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(__uint_as_float((uint32_t)max(132 + byte - top, 1) << 23)));
+          else asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(scale) : "f"(far ? 1.f : __uint_as_float((uint32_t)max(132 + byte - top, 1) << 23)));
           if (!which && a.scale < 0.f) scale ^= 0x80008000u;  // (so that the scores' factors are not negative)
           sh.scale[which][par][ct] = live ? scale : 0u;
-          if (which && ct == 0) sh.E[par] = unit - 127;
+          if (ct == 0) {
+            if (which) sh.E[par] = unit - 127;
+            else sh.s_exp[par] = far ? FAR : top - 127 - 5;
+          }
         }
-        if (!which && ct == 0) sh.s_exp[par] = top - 127 - 5;
         all_of<128>(2 + which, true);  // the scales are there
         // 16 codes a turn; eight neighbouring lanes take four pieces of two tokens, which the swizzle (16-byte pieces
         // exchanged by the row's number) puts into different banks

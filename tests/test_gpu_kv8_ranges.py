@@ -1,5 +1,5 @@
 """Attention over the 8-bit cache at the ends of its numbers: rows of q and keys whose sizes are far from 1 and whose
-scores are not, scales of 2^-127. Bounds: tests/kv8_bounds.py."""
+scores are not, keys far apart, scales of 2^-127. Bounds: tests/kv8_bounds.py."""
 
 import numpy as np
 import pytest
@@ -46,3 +46,19 @@ def test_a_scale_of_0_is_no_zero(type, step):
     o = c.attend(q, step=step)
     check(c, o, q.double().cpu().numpy(), rows=11)
     assert not torch.equal(o, c.attend(q * 0, step=step))
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("window", [0, 16])
+@pytest.mark.parametrize("bytes", [(121, 165, 119, 122, 120), (120, 120, 0, 120, 1), (119, 180, 100, 121, 120), (121, 121, 148, 121, 142)])
+def test_keys_far_apart(type, code, window, bytes):
+    """A row's scores do not depend on keys that it does not see, whatever their size."""
+    c = Cache([(0, 80), (300, 70)], H=4, G=2, D=64, page=16, block=16, type=type, code=code, window=window, seed=43)
+    for g in range(c.G):
+        for j, byte in enumerate(bytes):
+            for page in (c.table[0, j], c.table[1, 16 + j]):
+                c.scales_of(c.cache, page, g, 0)[:] = byte
+    c.upload()
+    q, qd = c.rows(c.H * c.D)
+    check(c, c.attend(q), qd)
