@@ -190,7 +190,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         x.row0 = (turn & 1 ? s.tiles - 1 - turn / 2 : turn / 2) * 8 * NT;
         x.g = g;
         x.first = s.past + x.row0 / a.rep;
-        x.final = s.past + (min(x.row0 + 8 * NT, s.n * a.rep) - 1) / a.rep;
+        x.final = s.past + (x.row0 + (kv8_rows_left(s.n * a.rep, x.row0, 8 * NT) - 1)) / a.rep;
         x.from = max(a.window ? max(x.first - a.window + 1, 0) : 0, s.base + j0 * GROUP);
         x.to = min(min(x.final + 1, s.end), s.base + j1 * GROUP);
         const long long gone = min((long long)s.groups + PAD - j0, left);
@@ -202,7 +202,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
       const int ps = k & 1;
       if (k > 1) ok = __all_sync(0xffffffffu, mbar_wait(&sh.piece_free[ps], (k >> 1) - 1 & 1));
       if (!ok) break;
-      const int rows = min(8 * NT, x.n * a.rep - x.row0);
+      const int rows = kv8_rows_left(x.n * a.rep, x.row0, 8 * NT);
       if (lane == 0) {
         sh.piece[ps] = x;
         mbar_arrive_expect_tx(&sh.piece_full[ps], x.groups ? rows * D * (int)sizeof(T) : 0);
@@ -322,7 +322,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
     }
     const Piece& pc = sh.piece[ps];
     if (pc.groups == 0) break;
-    const int row0 = pc.row0, rows = pc.n * a.rep, from = pc.from, to = pc.to, first = pc.first, final = pc.final;
+    const int row0 = pc.row0, rows = pc.n * a.rep - pc.row0, from = pc.from, to = pc.to, first = pc.first, final = pc.final;
 
     // ---- q ----
     uint32_t qf[QP][NT][KJ * 4][2];
@@ -341,7 +341,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const int at = (qt * KJ + j) * 16;
-          const bool in = row0 + 8 * n + qr < rows && (FULL || at < D);
+          const bool in = 8 * n + qr < rows && (FULL || at < D);
           const float4 v = in ? load4(q + at + 4 * w) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[j][4 * w] = v.x, x[j][4 * w + 1] = v.y, x[j][4 * w + 2] = v.z, x[j][4 * w + 3] = v.w;
 #pragma unroll
@@ -374,7 +374,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         const float factor = __shfl_sync(0xffffffffu, inv, (2 * qt + c) * 4);
         rf[n][c] = factor > 1.f ? 1.f : factor;
         rf2[n][c] = fminf(fmaxf(fmaxf(factor, 1.f) * a.scale * 1.44269504f, -3e38f), 3e38f);
-        pos[n][c] = pc.past + (row0 + 8 * n + 2 * qt + c) / a.rep;
+        pos[n][c] = pc.past + (row0 + min(8 * n + 2 * qt + c, rows - 1)) / a.rep;
       }
     }
 
@@ -629,7 +629,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
           continue;
         }
         int h = 0;
-        T* out = out_row<T>(a, pc.begin, pc.n, pc.g, row0 + r, h);
+        T* out = out_row<T>(a, pc.begin, pc.n, pc.g, row0, r, h);
         if (!out) continue;
         store4(out + d, row_scale(a, h, st), x);
       }

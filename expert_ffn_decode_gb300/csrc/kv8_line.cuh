@@ -2,6 +2,7 @@
 #pragma once
 
 #include "kv8.cuh"
+#include "kv8_rows.h"
 
 namespace moe {
 
@@ -43,7 +44,7 @@ __device__ __forceinline__ Seq seq_of(const Kv8Args& a, int b, int rows) {
   s.base = a.window ? max(s.past - a.window + 1, 0) & ~(GROUP - 1) : 0;
   s.end = max(s.end, s.base);
   const bool many = a.few_rows >= 0 && s.n * a.rep > a.few_rows;  // sequences of many rows have a kernel of their own
-  s.tiles = many == (GROUP >= 128) ? (s.n * a.rep + rows - 1) / rows : 0;
+  s.tiles = many == (GROUP >= 128) ? kv8_tiles(s.n * a.rep, rows) : 0;
   s.groups = max(1, (s.end - s.base + GROUP - 1) / GROUP);
   return s;
 }
@@ -150,11 +151,11 @@ __device__ __forceinline__ void store4(T* out, const RowScale& r, const float4& 
   if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
   else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
 }
-// Where a row of the sequence's tokens begin .. begin + n - 1 goes, or null.
+// Where row r of the tile from row0 on of the sequence's tokens begin .. begin + n - 1 goes, or null.
 template <typename T>
-__device__ __forceinline__ T* out_row(const Kv8Args& a, int begin, int n, int g, int row, int& h) {
-  if (row >= n * a.rep) return nullptr;
-  const int i = row / a.rep;
+__device__ __forceinline__ T* out_row(const Kv8Args& a, int begin, int n, int g, int row0, int r, int& h) {
+  if (r >= n * a.rep - row0) return nullptr;
+  const int row = row0 + r, i = row / a.rep;
   h = g * a.rep + row - i * a.rep;
   return static_cast<T*>(a.o) + (int64_t)(begin + i) * a.os + h * a.D;
 }
@@ -209,7 +210,7 @@ __device__ __forceinline__ void join(const Kv8Args& a, const Kv8Parts& f, int th
       continue;
     }
     int h = 0;
-    T* out = out_row<T>(a, begin, tokens, g, row0 + r, h);
+    T* out = out_row<T>(a, begin, tokens, g, row0, r, h);
     if (!out) continue;
     store4(out + d, row_scale(a, h, st), o);
   }

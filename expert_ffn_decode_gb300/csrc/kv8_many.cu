@@ -284,8 +284,8 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       const int first = pc.past + pc.row0 / a.rep + h * half_tokens;  // position of the tile's first row
       const int pos = first + r / a.rep;
       const int t_last = first + half_tokens - 1;  // of the tile's last row
-      const bool real = r < half_rows && pc.row0 + h * half_rows + r < pc.n * a.rep;
-      const bool tile_real = pc.row0 + h * half_rows < pc.n * a.rep;
+      const int left = pc.n * a.rep - pc.row0 - h * half_rows;  // rows from the tile's first on
+      const bool real = r < half_rows && r < left, tile_real = left > 0;
       float m = 0.f, l = 0.f;
       int q_exp = 0;  // rows of q are their operands times 2^q_exp
       bool fresh = true;  // has seen no token
@@ -508,7 +508,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       const bool own = pc.c0 == pc.c1;
       const int64_t at = (int64_t)(cta == pc.c0 ? pc.slot0 : 2 * cta) * f.rows + h * half_rows + r;
       int hd = 0;
-      T* out = real ? out_row<T>(a, pc.begin, pc.n, pc.g, pc.row0 + h * half_rows + r, hd) : nullptr;
+      T* out = real ? out_row<T>(a, pc.begin, pc.n, pc.g, pc.row0, h * half_rows + r, hd) : nullptr;
       RowScale rs{0.f, 1.f, 1.f};
       if (own) {
         if (!nothing && real) rs = row_scale(a, hd, Stats{m, (float)E, l, 0.f});
