@@ -259,7 +259,7 @@ int kv8_args(const Kv8Rows* rows, int n_rows, const void* cache, bool cache_out,
   a->capacity = c->max_pages * c->page_tokens;
   a->code = c->code;
   a->type = c->type;
-  a->window = c->window > (1 << 30) + (1 << 28) ? 0 : c->window;  // (no position is that far)
+  a->window = c->window;
   a->scale = c->scale;
   return MOE_OK;
 }

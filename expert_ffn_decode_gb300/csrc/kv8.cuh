@@ -23,6 +23,14 @@ __device__ __forceinline__ void kv8_range(const Kv8Args& a, int b, int& begin, i
 __device__ __forceinline__ int kv8_past(const Kv8Args& a, int b) {
   return a.past ? min(max(a.past[b], -(1 << 28)), 1 << 30) : 0;
 }
+// How many positions a row of sequence b sees, its own the last, with positions clamped as above: less by what was taken
+// from them (0 and fewer: none that can be held). No window: more than there are positions.
+__device__ __forceinline__ int kv8_window(const Kv8Args& a, int b) {
+  constexpr int all = (1 << 30) + (1 << 28) + 1;
+  if (!a.window) return all;
+  const int over = a.past ? max(a.past[b], 1 << 30) - (1 << 30) : 0;
+  return min(max(a.window - over, -(1 << 28)), all);
+}
 // The sequence that a row is a token of, or -1, by bisection of the ascending offsets.
 __device__ __forceinline__ int kv8_seq_of(const Kv8Args& a, int row, int& begin, int& end) {
   int b = 0;

@@ -103,7 +103,7 @@ struct FewPlan {
 struct Piece {
   int groups;                  // of the whole stretch of the line; 0: no more pieces
   int c0, c1, slot0;           // the CTAs that have parts of it, where the first of them keeps its own
-  int b, begin, n, past;       // sequence, its first row, tokens, position
+  int b, begin, n, past, window;  // sequence, its first row, tokens, position, positions that a row sees
   int row0, g;                 // the tile's first row, head
   int from, to, first, final;  // tokens that count here, positions of the tile's first and last row
 };
@@ -187,11 +187,12 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
         x.begin = s.begin;
         x.n = s.n;
         x.past = s.past;
+        x.window = s.window;
         x.row0 = (turn & 1 ? s.tiles - 1 - turn / 2 : turn / 2) * 8 * NT;
         x.g = g;
         x.first = s.past + x.row0 / a.rep;
         x.final = s.past + (x.row0 + (kv8_rows_left(s.n * a.rep, x.row0, 8 * NT) - 1)) / a.rep;
-        x.from = max(a.window ? max(x.first - a.window + 1, 0) : 0, s.base + j0 * GROUP);
+        x.from = max(max(x.first - s.window + 1, 0), s.base + j0 * GROUP);
         x.to = min(min(x.final + 1, s.end), s.base + j1 * GROUP);
         const long long gone = min((long long)s.groups + PAD - j0, left);
         line += gone;
@@ -388,7 +389,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
       for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
     // groups that every row sees whole
-    const int whole0 = max((from + GROUP - 1) / GROUP, a.window ? ((final - a.window) >> (U + 3)) + 1 : 0);
+    const int window = pc.window, whole0 = max((from + GROUP - 1) / GROUP, ((final - window) >> (U + 3)) + 1);
     const int whole1 = min((first + 1) / GROUP, to / GROUP);
     auto work = [&](int st, int held, int grp) {
       const uint8_t* src = ring + (warp * 2 + st) * P::STAGE;
@@ -442,7 +443,7 @@ kv8_few(Kv8Args a, Kv8Parts f, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int t = grp * GROUP + 16 * u + qr + 8 * (e >> 1), p = pos[n][e & 1];
-              if (!(held >> u & 1) || t < from || t >= to || t > p || (a.window && t <= p - a.window)) sc[u][n][e] = -INFINITY;
+              if (!(held >> u & 1) || t < from || t >= to || t > p || t <= p - window) sc[u][n][e] = -INFINITY;
             }
       }
       float w1[U][NT][4], wv[U][NT][4];  // weights in the sum, and as V's operands

@@ -22,7 +22,7 @@ constexpr float LOWEST = -3e38f;  // the reference of a row that has seen nothin
 // whatever its length (a cut among them counts as one behind them). Order: sequences, tiles (from both ends in turn, as
 // later ones see more), heads, groups.
 struct Seq {
-  int begin, n, past;  // first row, tokens, position of the first
+  int begin, n, past, window;  // first row, tokens, position of the first, positions that a row sees
   int base, end;       // tokens that any of its rows sees, from a multiple of GROUP on
   int tiles, groups;   // row tiles, groups of tokens
 };
@@ -41,7 +41,8 @@ __device__ __forceinline__ Seq seq_of(const Kv8Args& a, int b, int rows) {
   s.n = end - s.begin;
   s.past = kv8_past(a, b);
   s.end = min(s.past + s.n, a.capacity);
-  s.base = a.window ? max(s.past - a.window + 1, 0) & ~(GROUP - 1) : 0;
+  s.window = kv8_window(a, b);
+  s.base = max(s.past - s.window + 1, 0) & ~(GROUP - 1);
   s.end = max(s.end, s.base);
   const bool many = a.few_rows >= 0 && s.n * a.rep > a.few_rows;  // sequences of many rows have a kernel of their own
   s.tiles = many == (GROUP >= 128) ? kv8_tiles(s.n * a.rep, rows) : 0;

@@ -18,7 +18,7 @@
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
 // As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
-// takes 2.74 ms for a 16,384-token prompt where this takes 3.31, but has 11 bits down to 2^-17 of the largest weight, fewer
+// takes 2.74 ms for a 16,384-token prompt where this takes 3.34, but has 11 bits down to 2^-17 of the largest weight, fewer
 // below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
 // value, as in trained models.)
 //
@@ -60,7 +60,7 @@ struct Plan {
 struct Piece {
   int groups;                  // of the whole stretch of the line; 0: no more pieces
   int c0, c1, slot0;           // the CTAs that have parts of it, where the first of them keeps its own
-  int b, begin, n, past;       // sequence, its first row, tokens, position
+  int b, begin, n, past, window;  // sequence, its first row, tokens, position, positions that a row sees
   int row0, g;                 // the first of the rows, head
   int from, to;                // tokens that count here
   int g0, g1;                  // groups with some
@@ -270,7 +270,6 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
     const int h = warp >> 3, part = warp >> 2 & 1, r = tid & 127;  // tile, half of the tokens, row of the tile
     const uint32_t lanes = tm + ((uint32_t)(warp & 3) * 32u << 16);
     const uint32_t t_s = lanes + T_S + h * 128 + part * 64, t_o = lanes + T_O + h * 128;  // weights: over the first half of t_s
-    const int window = a.window ? a.window : 1 << 30;
     const float scale2 = fabsf(a.scale) * 1.44269504f;
     uint32_t group = 0, filled = 0;          // groups and pieces with some so far
     auto rows_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(SOFTMAX) : "memory"); };
@@ -282,7 +281,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       const Piece& pc = sh.piece[k & 1];
       if (pc.groups == 0) break;
       const int first = pc.past + pc.row0 / a.rep + h * half_tokens;  // position of the tile's first row
-      const int pos = first + r / a.rep;
+      const int pos = first + r / a.rep, from = max(pos - pc.window + 1, 0);  // of the tokens that the row sees
       const int t_last = first + half_tokens - 1;  // of the tile's last row
       const int left = pc.n * a.rep - pc.row0 - h * half_rows;  // rows from the tile's first on
       const bool real = r < half_rows && r < left, tile_real = left > 0;
@@ -338,9 +337,9 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.op_full[(2 * group + 1) % 3], (2 * group + 1) / 3 & 1));  // E is there
         const uint4 valid = *reinterpret_cast<const uint4*>(sh.valid[0][par]);
         const uint4 nk = *reinterpret_cast<const uint4*>(sh.nan[0][par]), nv = *reinterpret_cast<const uint4*>(sh.nan[1][par]);
-        const bool whole = (valid.x & valid.y & valid.z & valid.w) == ~0u && t0 + TOK - 1 <= first && t0 > t_last - window &&
+        const bool whole = (valid.x & valid.y & valid.z & valid.w) == ~0u && t0 + TOK - 1 <= first && t0 > t_last - pc.window &&
                            sh.s_exp[par] != FAR && (nk.x | nk.y | nk.z | nk.w | nv.x | nv.y | nv.z | nv.w) == 0;
-        if (!tile_real || t0 > t_last || t0 + TOK - 1 <= first - window) {  // the mask leaves the tile's rows nothing here
+        if (!tile_real || t0 > t_last || t0 + TOK - 1 <= first - pc.window) {  // the mask leaves the tile's rows nothing here
           uint32_t z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0;
@@ -350,7 +349,7 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           // which of 32 tokens from t0 + 64 part + 32 c on the row sees
           auto seen_of = [&](int c) {
             const int tc = t0 + part * 64 + c * 32;
-            const int lo = min(max(max(pos - window + 1, 0) - tc, 0), 32), hi = min(max(pos + 1 - tc, 0), 32);
+            const int lo = min(max(from - tc, 0), 32), hi = min(max(pos + 1 - tc, 0), 32);
             return sh.valid[0][par][part * 2 + c] & (uint32_t)((1ull << hi) - (1ull << min(lo, hi)));
           };
           const bool far = sh.s_exp[par] == FAR;  // (for all tokens of the group)
@@ -695,10 +694,11 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           x.begin = s.begin;
           x.n = s.n;
           x.past = s.past;
+          x.window = s.window;
           x.row0 = (turn & 1 ? s.tiles - 1 - turn / 2 : turn / 2) * f.rows;
           x.g = g;
           const int t = x.row0 / a.rep, first = s.past + t, final = s.past + min(t + 2 * half_tokens, s.n) - 1;
-          x.from = max(a.window ? max(first - a.window + 1, 0) : 0, s.base + j0 * TOK);
+          x.from = max(max(first - s.window + 1, 0), s.base + j0 * TOK);
           x.to = min(min(final + 1, s.end), s.base + j1 * TOK);
           x.g0 = x.from / TOK;
           x.g1 = x.from < x.to ? (x.to + TOK - 1) / TOK : x.g0;

@@ -1,5 +1,5 @@
 """Attention over the 8-bit cache at the ends of its numbers: rows of q and keys whose sizes are far from 1 and whose
-scores are not, keys far apart, scales of 2^-127. Bounds: tests/kv8_bounds.py."""
+scores are not, keys far apart, scales of 2^-127, positions far behind the table. Bounds: tests/kv8_bounds.py."""
 
 import numpy as np
 import pytest
@@ -62,3 +62,22 @@ def test_keys_far_apart(type, code, window, bytes):
     c.upload()
     q, qd = c.rows(c.H * c.D)
     check(c, c.attend(q), qd)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("past", [2 ** 30 - 100, 2 ** 30, 2 ** 30 + 5, 2 ** 31 - 1])
+@pytest.mark.parametrize("window", [0, 16, 2 ** 30 - 150, 2 ** 30 + 2, 2 ** 30 + 2 ** 28, 2 ** 30 + 2 ** 28 + 1, 2 ** 31 - 5, 2 ** 31 - 1])
+def test_positions_far_behind_the_table(type, past, window):
+    """A row at position p sees the held positions from p - window + 1 on, as one at position 1000 does with that first one."""
+    c = Cache([(0, 200), (40, 70)], H=4, G=2, D=64, page=16, block=4, type=type, window=window, seed=44).upload()
+    q, _ = c.rows(c.H * c.D)
+    first = past - window + 1 if window else None
+    c.d_past[:] = past
+    o = c.attend(q)
+    if first is not None and first > 1000:
+        assert not o.any()
+        return
+    c.d_past[:] = 1000
+    c.window = 1001 - first if window else 0
+    want = c.attend(q)
+    assert torch.equal(o, want) and (want[0] != 0).any() == (first is None or first < 208)
