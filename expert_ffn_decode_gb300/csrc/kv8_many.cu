@@ -11,14 +11,14 @@
 // K and V alternate through three places for codes and three for operands. Scales are powers of two and go into the
 // operands: K times 2^5 over the largest K scale of the 128 tokens as f16, exact for scales down to 2^-29 of that (of e4m3's
 // smallest codes to 2^-20; where one is smaller, no scale of the group goes in, and scores get theirs one by one), V as bf16 in units that depend on the largest V scale the CTA has seen for
-// the tiles: exact, whatever the others, while that one is below 2^25, and for scales down to 2^-140 of a larger one.
+// the tiles: exact, whatever the others, while that one is at most 2^49, and for scales down to 2^-170 of a larger one.
 // (Scales beside the operands, read from shared memory for each score, took 505 us where this took 395: 512 tokens x 32
 // heads behind 32,768.) bf16 rows of q become f16 ones in place, times a power of two a row.
-// Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 40 (powers of two); then,
+// Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 16 (powers of two); then,
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
 // As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
-// takes 2.74 ms for a 16,384-token prompt where this takes 3.34, but has 11 bits down to 2^-17 of the largest weight, fewer
+// takes 2.74 ms for a 16,384-token prompt where this takes 3.40, but has 11 bits down to 2^-17 of the largest weight, fewer
 // below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
 // value, as in trained models.)
 //
@@ -43,10 +43,10 @@ namespace {
 constexpr int TOK = 128;  // tokens of a group
 constexpr int SOFTMAX = 512, THREADS = SOFTMAX + 384;
 constexpr uint32_t HALF = 16384;  // 128 rows of 128 bytes: 64 dimensions of an operand of 128 rows
-constexpr float SLACK = 40.f;  // weights of up to 2^40
+constexpr float SLACK = 16.f;  // weights of up to 2^16: more would take from the powers below that parts and sinks are added by
 // V's operands are in units of 2^(unit - 127), unit a multiple of 16 that the largest scale byte is at most HEAD above: sums
 // of 2^30 weights of 2^SLACK times codes of 2^9 stay f32 numbers.
-constexpr int HEAD = 40;
+constexpr int HEAD = 64;
 constexpr int FAR = 1 << 20;
 constexpr uint32_t T_S = 0, T_O = 256;  // tensor memory: 128 columns a tile each
 

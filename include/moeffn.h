@@ -468,7 +468,8 @@ int moe_kv8_read(const void* cache, const int32_t* offsets, const int32_t* past,
  * Bits: scores, softmax statistics and sums are f32, o is rounded once. As operands the weights have 16 bits (bf16, and
  * f16 sequences of more than 48 rows: tokens x heads that share a key/value head) or 24 (the others), each by its own size,
  * however small it is beside the row's largest. V is exact; in sequences of more than 48 rows of 16-bit types and heads of up
- * to 128 while no V scale among a tile's tokens is above 2^25, else for scales down to 2^-140 of the largest. (Scores beyond f32's range are infinities
+ * to 128 while no V scale among a tile's tokens is above 2^49, else for scales down to 2^-170 of the largest. Weights below
+ * 2^-110 of the row's largest, or of its sink's, may be 0. (Scores beyond f32's range are infinities
  * and what their rows become is open.) A row of q that holds an infinity or a
  * NaN gives a row that is not finite, and so does a NaN block that a row sees; neither reaches other
  * rows. */

@@ -1,6 +1,7 @@
 """Attention over the 8-bit cache where nearly all weight is on tokens of next to no value: the others' weights
 keep their bits whatever their size. Bounds: tests/kv8_bounds.py, relative to sum p |v|."""
 
+import numpy as np
 import pytest
 
 from tests.kv8_bounds import behind, check, far_values, rows_of
@@ -46,3 +47,23 @@ def test_prompts_of_any_factor(type, scale):
     c = Cache([(200, 90), (0, 150)], D=64, type=type, seed=34).upload()
     q, qd = c.rows(c.H * c.D)
     check(c, c.attend(q, cfg=c.cfg(scale=scale)), qd, rows=11, scale=scale)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("rise", [0, 14, 38])
+def test_sinks_far_above(type, rise):
+    """A sink of 2^100 times all tokens' weight, where the later tokens' scores are `rise` powers of two above the first ones'."""
+    c = Cache([(0, 290)] * 40, H=4, G=2, D=64, type=type, sinks=True, spread=0.0, seed=35)  # (several groups a CTA)
+    for g in range(c.G):
+        for page in range(c.n_pages):
+            c.codes_of(c.cache, page, g, 0)[:, 0] = 0
+        for b in range(c.B):
+            for page in c.table[b, 2:]:
+                if page >= 0:
+                    c.codes_of(c.cache, page, g, 0)[:, 0] = 64
+    c.sinks[:] = (100 + rise) * np.log(2.0)
+    c.upload()
+    q = torch.from_numpy(c.rng.standard_normal((c.N, c.H, c.D))).cuda()
+    q[..., 0] = rise * np.log(2.0) * c.D ** 0.5
+    q = q.flatten(1).to(types()[type][1])
+    check(c, c.attend(q), q.double().cpu().numpy(), rows=71)
