@@ -165,7 +165,7 @@ __device__ __forceinline__ T* out_row(const Kv8Args& a, int begin, int n, int g,
 template <typename T, typename F>
 __device__ __forceinline__ void join(const Kv8Args& a, const Kv8Parts& f, int threads, int begin, int tokens, int row0,
                                      int g, int n, int to, F slot) {
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 4;  // parts in flight (eight take registers that the many-rows kernel's loop then lacks: 390 -> 417 us)
   const int per = f.rows * a.D / 4;
   for (int i0 = 0; i0 < per; i0 += threads) {
     const int i = min(i0 + (int)threadIdx.x, per - 1), r = i * 4 / a.D, d = i * 4 - r * a.D;

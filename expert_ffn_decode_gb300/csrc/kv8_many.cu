@@ -17,15 +17,18 @@
 // Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 16 (powers of two); then,
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
-// As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. (One f16 part
-// takes 2.74 ms for a 16,384-token prompt where this takes 3.40, but has 11 bits down to 2^-17 of the largest weight, fewer
-// below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all weight and next to no
-// value, as in trained models.)
+// As operands weights are two bf16 parts: 16 bits of each, however small it is beside the row's largest. Half of them
+// (32 of each thread's 64 tokens) are handed over at a time, so that their products, twice as many, run beside the others'
+// arithmetic. (One f16 part takes 2.74 ms for a 16,384-token prompt where this takes 3.12, but has 11 bits down to 2^-17 of
+// the largest weight, fewer below and none from 2^-28 on, which is where the tokens behind a first one are that has nearly all
+// weight and next to no value, as in trained models. Handed over all at once, 3.31.)
 //
-// No unit is full (counters of 512 tokens x 32 heads behind 32,768 tokens, 358 us: tensor pipe 36% of active cycles, issue
-// slots 46%, shared memory 31%): a tile's chain of products, weights and products is what a group's 5,500 cycles go into.
-// S in halves of 64 tokens with two places a tile, products beside weights, took 3.1 ms for 16,384 tokens where this takes
-// 2.73 (N = 64 reads q twice as often); all eight converting warps on K, then V, 2.92.
+// No unit is full (counters of 512 tokens x 32 heads behind 32,768 tokens, 367 us: issue slots 58%, tensor pipe 47%, shared
+// memory 34%): a tile's chain of products, weights and products is what a group's 6,300 cycles go into. Whole prompts wait
+// for their busiest CTA besides, as a tile's place on the line has the groups that any row of the sequence sees: 1,032
+// groups for 16,384 tokens where the mean is 869, twice the mean for 2,048 to 8,192 (145, 387 and 1,447 us).
+// With weights of one f16 part S in halves of 64 tokens with two places a tile, products beside weights, took 3.1 ms for
+// 16,384 tokens where one place took 2.73 (N = 64 reads q twice as often); all eight converting warps on K, then V, 2.92.
 //
 // The CTAs cut one line of all sequences' tiles, heads and groups of tokens into equal pieces, as in kv8_few.cuh.
 #include <cuda.h>
@@ -69,7 +72,7 @@ struct alignas(16) Shared {
   Scratch<THREADS / 32> scratch;
   Piece piece[2];
   uint64_t piece_full[2], piece_free[2], q_full, q_ready, q_free, raw_full[3], raw_free[3], op_full[3], op_free[3], s_full[2],
-      p_ready[2], o_full[2];
+      p_ready[2][2], o_full[2];
   uint32_t tmem;
   int top[2][2][4], low[2][4];     // largest scale byte of a warp's tokens, K and V, smallest of K
   int E[2];                        // of V for a group: what O is in units of
@@ -235,7 +238,8 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
       mbar_init(&sh.piece_full[i], 1);
       mbar_init(&sh.piece_free[i], SOFTMAX + 256 + 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], SOFTMAX / 2);
+      mbar_init(&sh.p_ready[i][0], SOFTMAX / 2);
+      mbar_init(&sh.p_ready[i][1], SOFTMAX / 2);
       mbar_init(&sh.o_full[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
@@ -345,6 +349,9 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           for (int i = 0; i < 16; ++i) z[i] = 0;
 #pragma unroll
           for (int c = 0; c < 64; c += 16) tmem_st16(t_s + c, z);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(&sh.p_ready[h][0]);
         } else {
           // which of 32 tokens from t0 + 64 part + 32 c on the row sees
           auto seen_of = [&](int c) {
@@ -437,6 +444,11 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
                   tmem_st8(t_s + c * 32 + y / 2, big);
                   tmem_st8(t_s + c * 32 + 16 + y / 2, small);
                 }
+                if (c == 0) {
+                  tmem_st_wait();
+                  tc_fence_before_sync();
+                  mbar_arrive(&sh.p_ready[h][0]);
+                }
               }
               const float2 both = add2(sum[0], sum[1]);
               l += both.x + both.y;
@@ -488,11 +500,14 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
               tmem_st16(t_s + c * 32 + 16, small);
             }
             l += more;
+            tmem_st_wait();
+            tc_fence_before_sync();
+            mbar_arrive(&sh.p_ready[h][0]);
           }
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&sh.p_ready[h]);
+        mbar_arrive(&sh.p_ready[h][1]);
       }
       // ---- the piece's rows: sums in units of 2^m, o of 2^E times that ----
       if (n_groups > 0) {
@@ -767,20 +782,19 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
         const uint32_t hi = (uint32_t)(q_desc >> 32);  // (of all)
         auto scores = [&](int h, uint32_t u) {
           const uint32_t q = (uint32_t)q_desc + h * (P::OPERAND >> 4), kk = (uint32_t)k_desc + u % 3 * (P::OPERAND >> 4);
-#pragma unroll
-          for (int s = 0; s < DP / 16; ++s)
-            if (s < steps)
+#pragma unroll 2
+          for (int s = 0; s < steps; ++s)
               mma_ss(tm + T_S + h * 128, q + ((s / 4) * HALF + (s % 4) * 32 >> 4), kk + ((s / 4) * HALF + (s % 4) * 32 >> 4), hi, s_desc, s > 0);
           mma_commit(&sh.s_full[h]);
         };
-        auto values = [&](int h, uint32_t u, bool first) {
+        auto values = [&](int h, uint32_t u, bool first, int c) {  // tokens 32 c .. 32 c + 31 of both halves
           const uint32_t v = (uint32_t)v_desc + u % 3 * (P::OPERAND >> 4);
-#pragma unroll
-          for (int s = 0; s < TOK / 16; ++s)
+#pragma unroll 2
+          for (int s = 0; s < 4; ++s)
 #pragma unroll
             for (int p = 1; p >= 0; --p)
-              mma_ts(tm + T_O + h * 128, tm + T_S + h * 128 + s / 2 * 32 + p * 16 + s % 2 * 8, v + (s * 2048 >> 4), hi, o_desc,
-                     !first || s > 0 || p == 0);
+              mma_ts(tm + T_O + h * 128, tm + T_S + h * 128 + s / 2 * 64 + c * 32 + p * 16 + s % 2 * 8,
+                     v + ((s / 2 * 4 + c * 2 + s % 2) * 2048 >> 4), hi, o_desc, !first || c > 0 || s > 0 || p == 0);
         };
         for (int k = 0; ok; ++k) {
           ok = mbar_wait(&sh.piece_full[k & 1], k >> 1 & 1);
@@ -799,17 +813,25 @@ kv8_many(Kv8Args a, Kv8Parts f, int half_tokens, const __grid_constant__ CUtenso
           for (int j = 0; j < n; ++j, unit += 2, ++group) {
             const bool more = j + 1 < n;
             op_ready(unit + 1);
-            ok = ok && mbar_wait(&sh.p_ready[0], group & 1);
+            ok = ok && mbar_wait(&sh.p_ready[0][0], group & 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            values(0, unit + 1, j == 0, 0);
+            ok = ok && mbar_wait(&sh.p_ready[0][1], group & 1);
             if (more) op_ready(unit + 2);
             if (!ok) break;
             tc_fence_after_sync();
-            values(0, unit + 1, j == 0);
+            values(0, unit + 1, j == 0, 1);
             if (more) scores(0, unit + 2);
             else mma_commit(&sh.o_full[0]);
-            ok = mbar_wait(&sh.p_ready[1], group & 1);
+            ok = mbar_wait(&sh.p_ready[1][0], group & 1);
             if (!ok) break;
             tc_fence_after_sync();
-            values(1, unit + 1, j == 0);
+            values(1, unit + 1, j == 0, 0);
+            ok = mbar_wait(&sh.p_ready[1][1], group & 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            values(1, unit + 1, j == 0, 1);
             mma_commit(&sh.op_free[(unit + 1) % 3]);
             if (more) {
               scores(1, unit + 2);
