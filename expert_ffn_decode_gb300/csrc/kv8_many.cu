@@ -10,10 +10,11 @@
 //   24, 25             the warp that copies (codes, q), the one that issues products
 // K and V alternate through three places for codes and three for operands. Scales are powers of two and go into the
 // operands: K times 2^5 over the largest K scale of the 128 tokens as f16, exact for scales down to 2^-29 of that (of e4m3's
-// smallest codes to 2^-20; where one is smaller, no scale of the group goes in, and scores get theirs one by one), V as bf16 in units that depend on the largest V scale the CTA has seen for
-// the tiles: exact, whatever the others, while that one is at most 2^49, and for scales down to 2^-170 of a larger one.
-// (Scales beside the operands, read from shared memory for each score, took 505 us where this took 395: 512 tokens x 32
-// heads behind 32,768.) bf16 rows of q become f16 ones in place, times a power of two a row.
+// smallest codes to 2^-20; where one is smaller, no scale of the group goes in, and scores get theirs one by one), V as bf16
+// in units that depend on the largest V scale the CTA has seen for the tiles: exact, whatever the others, while that one is at
+// most 2^49, and for scales down to 2^-170 of a larger one. (Scales beside the operands, read from shared memory for each
+// score, took 505 us where this took 395 with weights of one part: 512 tokens x 32 heads behind 32,768.) bf16 rows of q
+// become f16 ones in place, times a power of two a row.
 // Softmax keeps a reference m of a row's scores that is only raised when a score exceeds it by 16 (powers of two); then,
 // and when V's unit rises, the row of O is scaled in tensor memory. A group's scores are read twice: for the largest, which
 // says whether the reference does, and for the weights, which are made over them.
