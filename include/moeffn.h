@@ -449,7 +449,7 @@ size_t moe_kv8_page_bytes(const moe_kv8_cfg* cfg);
  * call's last one mean nothing any more. A call that starts at a block's first position takes no notice
  * of what the block held, so pages need no clearing. A block with an infinity or a NaN gets the
  * NaN scale, which makes all of its values NaN until its first position is written again.
- * Two sequences must not write to one block. */
+ * Two sequences must not write to one block, nor one sequence twice to a block of a page that its table has twice. */
 int moe_kv8_write(const void* k, const void* v, const int32_t* offsets, const int32_t* past, const int32_t* pages,
                   const moe_kv8_cfg* cfg, void* cache, void* stream);
 
