@@ -56,3 +56,33 @@ def test_many_heads_of_one_key(type, H):
     c = Cache([(0, 3), (200, 4), (17, 1), (0, 0), (1000, 2)], H=H, G=1, D=64, type=type, seed=54).upload()
     q, qd = c.rows(c.H * c.D)
     repeats(c, q, qd, False)
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_captured_prompts(type):
+    """A packed batch for both kernels, captured and replayed with other inputs and positions beside another call on another
+    stream, with and without programmatic launches: the same bits as calls one at a time."""
+    c = Cache([(500, 60), (0, 2), (30, 1), (0, 0), (900, 90)], H=8, G=2, D=64, type=type, seed=55).upload()
+    d = Cache([(2000, 3), (100, 200)], H=8, G=1, D=128, type=type, seed=56).upload()
+    (q, _), (q2, _) = c.rows(c.H * c.D), d.rows(d.H * d.D)
+    ws = torch.zeros(ffn.moe_kv8_workspace_size(c.cfg()), dtype=torch.uint8, device="cuda")
+    o, want2 = torch.empty_like(q), d.attend(q2)
+    side, graphs = torch.cuda.Stream(), []
+    for flags in (0, ffn.MOE_NO_PDL):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ffn.check(ffn.moe_kv8_attn_prefill(q, c.d_cache, c.d_offsets, c.d_past, c.d_table, None, c.cfg(flags=flags), o, ws,
+                                               ws.numel(), torch.cuda.current_stream()))
+    for t in range(3):
+        q.copy_(torch.randn(q.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(t)))
+        c.d_past.copy_(torch.tensor([500 - 100 * t, t, 30 + t, 0, 900 - 33 * t], dtype=torch.int32))
+        want = c.attend(q)
+        for g in graphs:
+            o.fill_(float("nan"))
+            torch.cuda.synchronize()
+            g.replay()
+            with torch.cuda.stream(side):
+                o2 = d.attend(q2)
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and torch.equal(o2, want2)
+    ffn.check(ffn.moe_workspace_status(ws, torch.cuda.current_stream()))
